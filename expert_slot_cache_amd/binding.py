@@ -31,6 +31,8 @@ POLICY_HOST, POLICY_DEVICE = 0, 1
 POLICIES = {"host": POLICY_HOST, "device": POLICY_DEVICE}
 EVICT_LRU, EVICT_FIFO, EVICT_LFU, EVICT_SLRU, EVICT_DECAY = 0, 1, 2, 3, 4
 EVICTS = {"lru": EVICT_LRU, "fifo": EVICT_FIFO, "lfu": EVICT_LFU, "slru": EVICT_SLRU, "decay": EVICT_DECAY}
+ROUTE_SOFTMAX, ROUTE_RENORM = 0, 1
+PRODUCT_F32, PRODUCT_BF16, PRODUCT_SWIGLU = 0, 1, 2
 PREFETCH_AFTER = {"layer": 0, "queued": 1, "previous": 2}
 
 
@@ -76,6 +78,7 @@ class Timing(C.Structure):
 
 _P = C.c_void_p
 _I32 = C.c_int32
+_I64 = C.c_int64
 _PI32 = C.POINTER(C.c_int32)
 
 _SIGS = {
@@ -107,6 +110,13 @@ _SIGS = {
     "moe_pool_set_slots": (_I32, [_P, _I32]),
     "moe_pool_set_eviction": (_I32, [_P, _I32]),
     "moe_forward_slots": (_I32, [_I32, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _I32, _P, _P]),
+    "moe_route": (_I32, [_I32, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_route_backward": (_I32, [_I32, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _P]),
+    "moe_sort_tokens": (_I32, [_I32, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, C.c_size_t, _P]),
+    "moe_sort_workspace_bytes": (C.c_size_t, [_I32, _I32, _I32]),
+    "moe_combine_rows": (_I32, [_I32, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P]),
+    "moe_combine_rows_backward": (_I32, [_I32, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_scaled_product": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "moe_lru_create": (_I32, [_I32, _I32, _I32, C.POINTER(_P)]),
     "moe_lru_destroy": (None, [_P]),
     "moe_lru_step": (_I32, [_P, _P, _I32, _I32, _P, C.POINTER(Miss), _I32, _PI32, _PI32]),
@@ -378,6 +388,194 @@ def is_pinned_host(addr: int) -> bool:
     v = C.c_int32(0)
     _check(lib().moe_ptr_is_pinned_host(addr, C.byref(v)))
     return bool(v.value)
+
+
+# ---- the operators around the experts ------------------------------------------------
+# On torch tensors of the current device, whose shapes give the sizes; every output is the
+# caller's buffer.  include/moe_pool.h documents each operator.
+
+
+def _bad(what: str):
+    raise MoeError(EINVAL, what)
+
+
+def _check_tensor(name: str, t, dtype, shape, dev: int, rows: bool = False):
+    """t lies on device `dev`, is of this dtype and shape, and contiguous (`rows`: only
+    within its rows)."""
+    if t.get_device() != dev:
+        _bad(f"{name} is not on the current device, cuda:{dev}")
+    if t.dtype is not dtype:
+        _bad(f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if rows:
+        if shape[1] > 1 and t.stride(1) != 1:
+            _bad(f"the values of a row of {name} are not contiguous")
+    elif not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+
+
+def _stride(t) -> int:
+    """Elements from one row to the next."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _atype(torch, name: str, t) -> int:
+    if t.dtype is torch.bfloat16:
+        return A_BF16
+    if t.dtype is torch.float32:
+        return A_F32
+    _bad(f"{name} is {t.dtype}, not float32 or bfloat16")
+
+
+def _matrix(name: str, t):
+    if t.dim() != 2:
+        _bad(f"{name} has {t.dim()} dimensions, not 2")
+    return t.shape
+
+
+def _place(torch, stream):
+    """The current device and the stream to use on it (torch's current one by default)."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream
+
+
+def route(logits, topk_ids, topk_w, *, renorm: bool = True, stream=None):
+    """moe_route: logits [T, E] (fp32 or bf16, rows may be apart) -> topk_ids int32 [T, K] and
+    topk_w fp32 [T, K]; renorm: the weights of a token sum to one."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, E = _matrix("logits", logits)
+    shape = (T, _matrix("topk_ids", topk_ids)[1])
+    _check_tensor("logits", logits, logits.dtype, logits.shape, dev, rows=True)
+    _check_tensor("topk_ids", topk_ids, torch.int32, shape, dev)
+    _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
+    _check(lib().moe_route(_atype(torch, "logits", logits), logits.data_ptr(), _stride(logits), T, E, shape[1],
+                           ROUTE_RENORM if renorm else ROUTE_SOFTMAX, topk_ids.data_ptr(), topk_w.data_ptr(), s))
+
+
+def route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, *, renorm: bool = True, stream=None):
+    """moe_route_backward: d_topk_w fp32 [T, K] -> d_logits [T, E] in the logits' type, for what
+    route gave on these logits (with renorm they are not read and may be None)."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, E = _matrix("d_logits", d_logits)
+    shape = (T, _matrix("topk_ids", topk_ids)[1])
+    _check_tensor("d_logits", d_logits, d_logits.dtype, d_logits.shape, dev, rows=True)
+    if logits is not None:
+        _check_tensor("logits", logits, d_logits.dtype, d_logits.shape, dev, rows=True)
+    _check_tensor("topk_ids", topk_ids, torch.int32, shape, dev)
+    _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
+    _check_tensor("d_topk_w", d_topk_w, torch.float32, shape, dev)
+    _check(lib().moe_route_backward(_atype(torch, "d_logits", d_logits), _ptr(logits),
+                                    E if logits is None else _stride(logits), topk_ids.data_ptr(), topk_w.data_ptr(),
+                                    d_topk_w.data_ptr(), T, E, shape[1], ROUTE_RENORM if renorm else ROUTE_SOFTMAX,
+                                    d_logits.data_ptr(), _stride(d_logits), s))
+
+
+def sort_workspace_bytes(n_tokens: int, top_k: int, experts: int) -> int:
+    return int(lib().moe_sort_workspace_bytes(n_tokens, top_k, experts))
+
+
+def sort_tokens(x, topk_ids, sorted_x, offsets, rows, *, scales=None, workspace=None, stream=None):
+    """moe_sort_tokens: x [T, H] (fp32 or bf16, rows may be apart) and topk_ids int32 [T, K] ->
+    sorted_x [T*K, H] (x's type, or float8_e4m3fn with scales fp32 [T*K, ceil(H/128)]), offsets
+    int32 [experts + 1] and rows int32 [T, K].  x and sorted_x None: the places only.
+    workspace: uint8, sort_workspace_bytes(T, K, experts) of them; None: taken from torch's
+    allocator for this call (on torch's current stream only)."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, K = _matrix("topk_ids", topk_ids)
+    _check_tensor("topk_ids", topk_ids, torch.int32, (T, K), dev)
+    _check_tensor("rows", rows, torch.int32, (T, K), dev)
+    E = offsets.numel() - 1
+    _check_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
+    H = at = f8 = stride = 0
+    if x is not None:
+        H = _matrix("x", x)[1]
+        at, stride = _atype(torch, "x", x), _stride(x)
+        _check_tensor("x", x, x.dtype, (T, H), dev, rows=True)
+        f8 = int(scales is not None)
+        _check_tensor("sorted_x", sorted_x, torch.float8_e4m3fn if f8 else x.dtype, (T * K, H), dev)
+        if f8:
+            _check_tensor("scales", scales, torch.float32, (T * K, -(-H // 128)), dev)
+    L = lib()
+    need = L.moe_sort_workspace_bytes(T, K, E)
+    if workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, workspace.shape, dev)
+        need = workspace.numel()
+    elif need:
+        if stream is not None and stream != torch.cuda.current_stream(dev).cuda_stream:
+            _bad("a sort on a stream that is not torch's current one needs its workspace from the caller")
+        workspace = torch.empty(need, dtype=torch.uint8, device=topk_ids.device)
+    _check(L.moe_sort_tokens(at, _ptr(x), stride, topk_ids.data_ptr(), T, K, E, H, f8, _ptr(sorted_x), _ptr(scales),
+                             offsets.data_ptr(), rows.data_ptr(), _ptr(workspace), need, s))
+
+
+def combine_rows(ys, rows, out, *, topk_w=None, resid=None, stream=None):
+    """moe_combine_rows: ys [T*K, H] (fp32 or bf16) at rows int32 [T, K], times topk_w fp32 [T, K]
+    (None: ones), summed with resid [T, H] (optional) into out [T, H].  Without weights it is
+    the gradient of sort_tokens."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, K = _matrix("rows", rows)
+    H = _matrix("out", out)[1]
+    _check_tensor("rows", rows, torch.int32, (T, K), dev)
+    _check_tensor("out", out, out.dtype, (T, H), dev)
+    _check_tensor("ys", ys, out.dtype, (T * K, H), dev)
+    if topk_w is not None:
+        _check_tensor("topk_w", topk_w, torch.float32, (T, K), dev)
+    if resid is not None:
+        _check_tensor("resid", resid, out.dtype, (T, H), dev)
+    _check(lib().moe_combine_rows(_atype(torch, "out", out), ys.data_ptr(), rows.data_ptr(), _ptr(topk_w), _ptr(resid),
+                                  T, K, H, out.data_ptr(), s))
+
+
+def combine_rows_backward(d_out, ys, rows, topk_w, d_ys, d_topk_w, *, stream=None):
+    """moe_combine_rows_backward: d_out [T, H] -> d_ys [T*K, H] (rows that no pair has are left as
+    they are) and d_topk_w fp32 [T, K], for what combine_rows took."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, K = _matrix("rows", rows)
+    H = _matrix("d_out", d_out)[1]
+    _check_tensor("rows", rows, torch.int32, (T, K), dev)
+    _check_tensor("d_out", d_out, d_out.dtype, (T, H), dev)
+    _check_tensor("ys", ys, d_out.dtype, (T * K, H), dev)
+    _check_tensor("d_ys", d_ys, d_out.dtype, (T * K, H), dev)
+    _check_tensor("topk_w", topk_w, torch.float32, (T, K), dev)
+    _check_tensor("d_topk_w", d_topk_w, torch.float32, (T, K), dev)
+    _check(lib().moe_combine_rows_backward(_atype(torch, "d_out", d_out), d_out.data_ptr(), ys.data_ptr(),
+                                           rows.data_ptr(), topk_w.data_ptr(), T, K, H, d_ys.data_ptr(),
+                                           d_topk_w.data_ptr(), s))
+
+
+def scaled_product(x, x_scales, w, w_scales, out, *, offsets=None, swiglu_scales=None, stream=None):
+    """moe_scaled_product: rows x [M, K] (float8_e4m3fn, x_scales fp32 [M, ceil(K/128)]), sorted by
+    group as offsets int32 [G + 1] says (None: one group), times w [G, N, K] (float8_e4m3fn,
+    w_scales fp32 [G, ceil(N/128), ceil(K/128)]) into out [M, N], fp32 or bf16.  With
+    swiglu_scales fp32 [M, N/256]: out is float8_e4m3fn [M, N/2], silu(gate) * up rounded."""
+    import torch
+    dev, s = _place(torch, stream)
+    M, K = _matrix("x", x)
+    if w.dim() != 3:
+        _bad(f"w has {w.dim()} dimensions, not 3")
+    G, N, _ = w.shape
+    f8, f32, kb = torch.float8_e4m3fn, torch.float32, -(-K // 128)
+    _check_tensor("x", x, f8, (M, K), dev)
+    _check_tensor("x_scales", x_scales, f32, (M, kb), dev)
+    _check_tensor("w", w, f8, (G, N, K), dev)
+    _check_tensor("w_scales", w_scales, f32, (G, -(-N // 128), kb), dev)
+    if offsets is not None:
+        _check_tensor("offsets", offsets, torch.int32, (G + 1,), dev)
+    if swiglu_scales is not None:
+        ep = PRODUCT_SWIGLU
+        _check_tensor("out", out, f8, (M, N // 2), dev)
+        _check_tensor("swiglu_scales", swiglu_scales, f32, (M, N // 256), dev)
+    else:
+        ep = PRODUCT_BF16 if _atype(torch, "out", out) == A_BF16 else PRODUCT_F32
+        _check_tensor("out", out, out.dtype, (M, N), dev)
+    _check(lib().moe_scaled_product(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), _ptr(offsets),
+                                    M, G, N, K, ep, out.data_ptr(), _ptr(swiglu_scales), s))
 
 
 class SlotLRU:

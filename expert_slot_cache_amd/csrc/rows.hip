@@ -1,0 +1,565 @@
+// Tokens sorted by expert and back, and the gradient.
+//
+//   rows[t][k]    = place of pair (t, k) among the pairs with an id in [0, E), sorted by
+//                   id and, within an id, in (t, k) order; -1 for any other id
+//   offsets[e]    = rows of the experts before e; offsets[E] = rows in all
+//   sorted[rows[t][k]] = x[t], or its e4m3 codes with a power-of-two scale per 128 values
+//   out[t]        = resid[t] + sum_k w[t][k] ys[rows[t][k]]     (k in order, fp32)
+//   d_ys[rows[t][k]] = w[t][k] d_out[t],   d_w[t][k] = <d_out[t], ys[rows[t][k]]>
+//
+// The sort is a counting sort without atomics on positions, so it is stable and gives the
+// same places every time: a wave ranks its 64 pairs by matching ids over ballots (one per
+// bit of an id), waves and workgroups take their turn through prefix sums of the counts.
+// Everything else moves rows: a token is read once for all of its K copies.
+#include <hip/hip_runtime.h>
+
+#include "ops.hpp"
+#include "ops_dev.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kRounds = 4;                         // pairs per lane and pass of a workgroup
+constexpr int kPass = kThreads * kRounds;          // pairs a workgroup ranks at a time
+constexpr int kMaxBlocks = 256;                    // workgroups of the two-launch sort
+// Pairs up to which every workgroup of the one launch sorts them all for itself.
+constexpr int kOneLaunch = kPass;
+
+// Pairs per workgroup of the two-launch sort (whole passes, at most kMaxBlocks workgroups).
+__host__ __device__ inline int64_t sort_chunk(int64_t P) {
+    const int64_t passes = (P + kPass - 1) / kPass;
+    return (passes + kMaxBlocks - 1) / kMaxBlocks * kPass;
+}
+
+// Dynamic LDS: base[E] int32, then cnt[kWaves][E] uint16.
+size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2 + 16; }
+
+// Exclusive prefix sums of v[0 .. E) in place, by the whole workgroup; returns the sum.
+__device__ int block_scan(int32_t* v, int E) {
+    __shared__ int wave_total[kWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int per = (E + kThreads - 1) / kThreads;
+    const int e0 = min(tid * per, E), e1 = min(e0 + per, E);
+    int own = 0;
+    for (int e = e0; e < e1; ++e) own += v[e];
+    int incl = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 63) wave_total[wave] = incl;
+    __syncthreads();
+    int at = incl - own, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        at += i < wave ? wave_total[i] : 0;
+        all += wave_total[i];
+    }
+    for (int e = e0; e < e1; ++e) {
+        const int c = v[e];
+        v[e] = at;
+        at += c;
+    }
+    __syncthreads();
+    return all;
+}
+
+// One pass of ranking: the workgroup's pairs p0 .. p0 + kPass, wave by wave, 64 at a time.
+// id[r] (-1: not a pair of any expert) and rank[r] (the pair's place among this wave's of
+// its expert so far); cnt[wave][e] ends as the wave's count.  No barrier inside.
+__device__ __forceinline__ void rank_pass(const int32_t* __restrict__ ids, int64_t p0, int64_t end, int E, int bits,
+                                          uint16_t* cnt, int id[kRounds], int rank[kRounds]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t first = p0 + (int64_t)wave * (kRounds * 64) + lane;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int64_t p = first + r * 64;
+        const int v = p < end ? ids[p] : -1;
+        id[r] = (unsigned)v < (unsigned)E ? v : -1;
+    }
+    uint16_t* mine = cnt + wave * E;
+    for (int e = lane; e < E; e += 64) mine[e] = 0;
+    __builtin_amdgcn_wave_barrier();   // LDS operations of one wave complete in order
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        uint64_t same = __ballot(id[r] >= 0);
+        for (int b = 0; b < bits; ++b) {
+            const bool one = (id[r] >> b) & 1;
+            const uint64_t m = __ballot(one);
+            same &= one ? m : ~m;
+        }
+        rank[r] = 0;
+        if (id[r] >= 0) {
+            const int before = lanes_below(same);
+            const int sofar = mine[id[r]];
+            rank[r] = sofar + before;
+            __builtin_amdgcn_wave_barrier();
+            if (before == 0) mine[id[r]] = (uint16_t)(sofar + __popcll(same));
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// After a barrier: cnt[wave][e] becomes the count of the waves before, base[e] moves past
+// this pass, and the return value of place() is a pair's row.
+__device__ __forceinline__ void waves_turn(int32_t* base, uint16_t* cnt, int E, bool advance) {
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        int sum = 0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+            const int c = cnt[i * E + e];
+            cnt[i * E + e] = (uint16_t)sum;
+            sum += c;
+        }
+        if (advance) base[e] = sum;
+    }
+}
+
+// ---- a token's row to its K places -----------------------------------------------------
+// bx lanes side by side (a power of two) walk the row; rows: the token's K places.
+// Copies: 16-byte pieces when `wide`, else one element at a time.
+template <int AT>
+__device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, bool wide, const int32_t* rows, int K,
+                                         int64_t P, void* out, int c, int bx) {
+    constexpr int es = AT == A_F32 ? 4 : 2;
+    if (wide) {
+        const char* src = static_cast<const char*>(x) + row * es;
+        const int n = H * es / 16;
+        for (; c < n; c += bx) {
+            const uint4 q = reinterpret_cast<const uint4*>(src)[c];
+            for (int k = 0; k < K; ++k) {
+                const int r = rows[k];
+                if (r >= 0) *reinterpret_cast<uint4*>(static_cast<char*>(out) + ((int64_t)r * H * es + (int64_t)c * 16)) = q;
+            }
+        }
+        return;
+    }
+    for (; c < H; c += bx) {
+        if constexpr (AT == A_F32) {
+            const float v = static_cast<const float*>(x)[row + c];
+            for (int k = 0; k < K; ++k)
+                if (rows[k] >= 0) static_cast<float*>(out)[(int64_t)rows[k] * H + c] = v;
+        } else {
+            const uint16_t v = static_cast<const uint16_t*>(x)[row + c];
+            for (int k = 0; k < K; ++k)
+                if (rows[k] >= 0) static_cast<uint16_t*>(out)[(int64_t)rows[k] * H + c] = v;
+        }
+    }
+}
+
+// e4m3: a lane takes 16 values, eight lanes side by side a block of 128 (bx is a multiple
+// of 8, H of 16; a last block may be shorter).
+template <int AT>
+__device__ __forceinline__ void round_row(const void* x, int64_t row, int H, bool wide, const int32_t* rows, int K,
+                                          uint8_t* out, float* scales, int c, int bx) {
+    const int n = H / 16, nb = (H + kBlock - 1) / kBlock;
+    const int steps = (n + bx - 1) / bx;   // every lane takes part in every step's exchange
+    for (int s = 0; s < steps; ++s, c += bx) {
+        float v[16];
+        if (c < n) {
+            if (wide) {
+                if constexpr (AT == A_F32) {
+                    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + row) + c * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 q = p[i];
+                        v[4 * i] = __uint_as_float(q.x);
+                        v[4 * i + 1] = __uint_as_float(q.y);
+                        v[4 * i + 2] = __uint_as_float(q.z);
+                        v[4 * i + 3] = __uint_as_float(q.w);
+                    }
+                } else {
+                    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + row) + c * 2;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 q = p[i];
+                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            v[8 * i + 2 * j] = widen_bf16((uint16_t)u[j]);
+                            v[8 * i + 2 * j + 1] = widen_bf16((uint16_t)(u[j] >> 16));
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = load_one<AT>(x, (size_t)row + (size_t)c * 16 + i);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+        }
+        float big = 0.0f;   // of the finite values: a NaN or an infinity poisons its own code alone
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float a = fabsf(v[i]);
+            if (a < __builtin_inff()) big = fmaxf(big, a);
+            else v[i] = __builtin_nanf("");
+        }
+        big = fmaxf(big, __shfl_xor(big, 1));
+        big = fmaxf(big, __shfl_xor(big, 2));
+        big = fmaxf(big, __shfl_xor(big, 4));
+        if (c >= n) continue;
+        const float scale = f8_scale(big), inv = f8_inverse(scale);
+        uint4 q;
+        q.x = f8_pack(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        q.y = f8_pack(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+        q.z = f8_pack(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv);
+        q.w = f8_pack(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv);
+        for (int k = 0; k < K; ++k) {
+            const int64_t r = rows[k];
+            if (r < 0) continue;
+            *reinterpret_cast<uint4*>(out + r * H + (int64_t)c * 16) = q;
+            if ((c & 7) == 0) scales[r * nb + (c >> 3)] = scale;
+        }
+    }
+}
+
+struct Spread {
+    const void* x;
+    int64_t stride;
+    int T, K, H, bx;
+    bool wide;
+    void* out;
+    float* scales;
+};
+
+template <int AT, bool F8>
+__device__ __forceinline__ void spread_token(const Spread& a, int64_t t, const int32_t* rows, int c) {
+    if constexpr (F8) round_row<AT>(a.x, t * a.stride, a.H, a.wide, rows, a.K, static_cast<uint8_t*>(a.out), a.scales, c, a.bx);
+    else copy_row<AT>(a.x, t * a.stride, a.H, a.wide, rows, a.K, (int64_t)a.T * a.K, a.out, c, a.bx);
+}
+
+// At most kOneLaunch pairs: every workgroup sorts them all (a few microseconds of ballots,
+// less than a launch and the wait for it), the first writes rows and offsets, and each
+// spreads its own tokens from the places it found.
+template <int AT, bool F8>
+__global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* __restrict__ ids, int E, int bits,
+        int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
+    extern __shared__ int32_t lds[];
+    __shared__ int32_t place[kOneLaunch];
+    int32_t* base = lds;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(lds + E);
+    const int P = a.T * a.K;
+    int id[kRounds], rank[kRounds];
+    rank_pass(ids, 0, P, E, bits, cnt, id, rank);
+    __syncthreads();
+    waves_turn(base, cnt, E, true);
+    __syncthreads();
+    const int all = block_scan(base, E);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+        const int p = wave * (kRounds * 64) + r * 64 + lane;
+        if (p < P) {
+            const int v = id[r] >= 0 ? base[id[r]] + cnt[wave * E + id[r]] + rank[r] : -1;
+            place[p] = v;
+            if (blockIdx.x == 0) rows[p] = v;
+        }
+    }
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < E; e += kThreads) offsets[e] = base[e];
+        if (threadIdx.x == 0) offsets[E] = all;
+    }
+    __syncthreads();
+    if (!a.x) return;
+    const int by = kThreads / a.bx;
+    const int t = blockIdx.x * by + threadIdx.x / a.bx;
+    if (t < a.T) spread_token<AT, F8>(a, t, place + t * a.K, threadIdx.x & (a.bx - 1));
+}
+
+// More pairs: counts per workgroup, then places, then the rows (a launch each).
+__global__ __launch_bounds__(kThreads) void k_sort_count(const int32_t* __restrict__ ids, int64_t P, int64_t chunk, int E,
+        int32_t* __restrict__ counts) {
+    extern __shared__ int32_t lds[];
+    for (int e = threadIdx.x; e < E; e += kThreads) lds[e] = 0;
+    __syncthreads();
+    const int64_t p0 = blockIdx.x * chunk, end = p0 + chunk < P ? p0 + chunk : P;
+    for (int64_t p = p0 + threadIdx.x; p < end; p += kThreads) {
+        const int v = ids[p];
+        if ((unsigned)v < (unsigned)E) atomicAdd(&lds[v], 1);   // counts: the order does not matter
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) counts[(int64_t)blockIdx.x * E + e] = lds[e];
+}
+
+__global__ __launch_bounds__(kThreads) void k_sort_place(const int32_t* __restrict__ ids, int64_t P, int64_t chunk, int E,
+        int bits, const int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
+    extern __shared__ int32_t lds[];
+    int32_t* base = lds;
+    uint16_t* cnt = reinterpret_cast<uint16_t*>(lds + E);
+    const int nb = gridDim.x, b = blockIdx.x;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        int sum = 0;
+        for (int i = 0; i < nb; ++i) sum += counts[(int64_t)i * E + e];
+        base[e] = sum;
+    }
+    __syncthreads();
+    const int all = block_scan(base, E);
+    if (b == 0) {
+        for (int e = threadIdx.x; e < E; e += kThreads) offsets[e] = base[e];
+        if (threadIdx.x == 0) offsets[E] = all;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += kThreads) {   // this workgroup's first row of each expert
+        int before = 0;
+        for (int i = 0; i < b; ++i) before += counts[(int64_t)i * E + e];
+        base[e] += before;
+    }
+    const int64_t p0 = b * chunk, end = p0 + chunk < P ? p0 + chunk : P;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t q0 = p0; q0 < end; q0 += kPass) {
+        int id[kRounds], rank[kRounds];
+        rank_pass(ids, q0, end, E, bits, cnt, id, rank);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int64_t p = q0 + wave * (kRounds * 64) + r * 64 + lane;
+            if (p >= end) continue;
+            int v = -1;
+            if (id[r] >= 0) {
+                v = base[id[r]] + rank[r];
+                for (int i = 0; i < wave; ++i) v += cnt[i * E + id[r]];
+            }
+            rows[p] = v;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) sum += cnt[i * E + e];
+            base[e] += sum;
+        }
+        __syncthreads();
+    }
+}
+
+template <int AT, bool F8>
+__global__ __launch_bounds__(kThreads) void k_spread(Spread a, const int32_t* __restrict__ rows) {
+    const int by = kThreads / a.bx;
+    int64_t t = (int64_t)blockIdx.x * by + threadIdx.x / a.bx;
+    if (a.bx >= 64) t = __builtin_amdgcn_readfirstlane((int)t);   // one token per wave: its places are scalars
+    if (t < a.T) spread_token<AT, F8>(a, t, rows + t * a.K, threadIdx.x & (a.bx - 1));
+}
+
+// ---- back: the weighted sum -------------------------------------------------------------
+template <int AT, bool WIDE>
+struct Piece {
+    static constexpr int N = WIDE ? (AT == A_F32 ? 4 : 8) : 1;
+    float v[N];
+    __device__ __forceinline__ void load(const void* p, int64_t i) {   // i: element index
+        if constexpr (WIDE) {
+            const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (AT == A_F32 ? 4 : 2));
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = AT == A_F32 ? __uint_as_float(u[j & 3]) : widen_bf16((uint16_t)(u[j >> 1] >> (16 * (j & 1))));
+        } else {
+            v[0] = load_one<AT>(p, (size_t)i);
+        }
+    }
+    __device__ __forceinline__ void store(void* p, int64_t i) const {
+        if constexpr (WIDE) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (AT == A_F32) u[j] = __float_as_uint(v[j]);
+                else u[j] = round_bf16(v[2 * j]) | (uint32_t)round_bf16(v[2 * j + 1]) << 16;
+            }
+            *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * (AT == A_F32 ? 4 : 2)) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+            store_one<AT>(p, (size_t)i, v[0]);
+        }
+    }
+};
+
+template <int AT, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restrict__ ys, const int32_t* __restrict__ rows,
+        const float* __restrict__ w, const void* __restrict__ resid, int T, int K, int H, int bx, void* __restrict__ out) {
+    using V = Piece<AT, WIDE>;
+    constexpr int KU = 8;   // rows in flight per lane
+    const int by = kThreads / bx;
+    int t = blockIdx.x * by + threadIdx.x / bx;
+    if (bx >= 64) t = __builtin_amdgcn_readfirstlane(t);
+    const int c = (blockIdx.y * bx + (threadIdx.x & (bx - 1))) * V::N;
+    if (t >= T || c >= H) return;
+    const unsigned P = (unsigned)T * (unsigned)K;
+    V acc;
+#pragma unroll
+    for (int i = 0; i < V::N; ++i) acc.v[i] = 0.0f;
+    for (int k0 = 0; k0 < K; k0 += KU) {
+        V y[KU];
+        bool on[KU];
+        float wk[KU];
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+            const int k = k0 + j;
+            const int r = k < K ? rows[(int64_t)t * K + k] : -1;
+            on[j] = (unsigned)r < P;   // any other place: a pair that went to no expert
+            wk[j] = on[j] && w ? w[(int64_t)t * K + k] : 1.0f;
+            if (on[j]) y[j].load(ys, (int64_t)r * H + c);
+        }
+#pragma unroll
+        for (int j = 0; j < KU; ++j)
+            if (on[j])
+#pragma unroll
+                for (int i = 0; i < V::N; ++i) acc.v[i] += wk[j] * y[j].v[i];
+    }
+    if (resid) {
+        V r;
+        r.load(resid, (int64_t)t * H + c);
+#pragma unroll
+        for (int i = 0; i < V::N; ++i) acc.v[i] += r.v[i];
+    }
+    acc.store(out, (int64_t)t * H + c);
+}
+
+// A wave takes a token and up to eight of its pairs (grid.y walks the groups of pairs):
+// d_out[t] is read once for them, each pair's dot product stays in a register per lane and
+// is summed over the wave at the end, in a fixed order.
+template <int AT, bool WIDE>
+__global__ __launch_bounds__(kThreads) void k_combine_rows_backward(const void* __restrict__ dout,
+        const void* __restrict__ ys, const int32_t* __restrict__ rows, const float* __restrict__ w, int T, int K, int per,
+        int H, void* __restrict__ dys, float* __restrict__ dw) {
+    using V = Piece<AT, WIDE>;
+    constexpr int KU = 8;
+    const int lane = threadIdx.x & 63;
+    const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
+    if (t >= T) return;
+    const int k0 = blockIdx.y * per, n = min(per, K - k0);
+    const unsigned P = (unsigned)T * (unsigned)K;
+    int64_t at[KU];
+    float wk[KU], dot[KU];
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+        const int64_t p = (int64_t)t * K + k0 + j;
+        const int r = j < n ? rows[p] : -1;
+        at[j] = (unsigned)r < P ? (int64_t)r * H : -1;
+        wk[j] = at[j] >= 0 ? w[p] : 0.0f;
+        dot[j] = 0.0f;
+    }
+    for (int c = lane * V::N; c < H; c += 64 * V::N) {
+        V d, y[KU];
+        d.load(dout, (int64_t)t * H + c);
+#pragma unroll
+        for (int j = 0; j < KU; ++j)
+            if (at[j] >= 0) y[j].load(ys, at[j] + c);
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+            if (at[j] < 0) continue;
+            V o;
+#pragma unroll
+            for (int i = 0; i < V::N; ++i) {
+                dot[j] += y[j].v[i] * d.v[i];
+                o.v[i] = wk[j] * d.v[i];
+            }
+            o.store(dys, at[j] + c);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+        if (j >= n) break;
+        const float sum = wave_sum(dot[j]);
+        if (lane == 0) dw[(int64_t)t * K + k0 + j] = sum;
+    }
+}
+
+int bits_of(int E) {
+    int b = 0;
+    while ((1 << b) < E) ++b;
+    return b;
+}
+// Lanes that share a row of n pieces: a power of two in [lo, 256].
+int lanes_for(int n, int lo) {
+    int bx = lo;
+    while (bx < n && bx < kThreads) bx *= 2;
+    return bx;
+}
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+template <int AT, bool F8>
+hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, int32_t* rows, int32_t* counts,
+                hipStream_t s) {
+    Spread a = a0;
+    constexpr int es = AT == A_F32 ? 4 : 2;
+    a.wide = on16(a.x) && a.stride * es % 16 == 0 && (F8 || (on16(a.out) && (int64_t)a.H * es % 16 == 0));
+    a.bx = F8 ? lanes_for(a.H / 16, 8) : lanes_for(a.wide ? a.H * es / 16 : a.H, 8);
+    const int64_t P = (int64_t)a.T * a.K;
+    const int bits = bits_of(E);
+    const int by = kThreads / a.bx;
+    const int tokens_grid = (a.T + by - 1) / by;
+    if (P <= kOneLaunch) {
+        hipLaunchKernelGGL((k_sort_one<AT, F8>), dim3(a.x ? tokens_grid : 1), dim3(kThreads), sort_lds(E), s, a, ids, E,
+                           bits, offsets, rows);
+        return hipGetLastError();
+    }
+    const int64_t chunk = sort_chunk(P);
+    const int nb = (int)((P + chunk - 1) / chunk);
+    hipLaunchKernelGGL(k_sort_count, dim3(nb), dim3(kThreads), (size_t)E * 4, s, ids, P, chunk, E, counts);
+    hipLaunchKernelGGL(k_sort_place, dim3(nb), dim3(kThreads), sort_lds(E), s, ids, P, chunk, E, bits, counts, offsets,
+                       rows);
+    if (a.x) hipLaunchKernelGGL((k_spread<AT, F8>), dim3(tokens_grid), dim3(kThreads), 0, s, a, rows);
+    return hipGetLastError();
+}
+
+template <int AT, bool WIDE>
+hipError_t combine(const void* ys, const int32_t* rows, const float* w, const void* resid, int T, int K, int H,
+                   void* out, hipStream_t s) {
+    const int n = H / Piece<AT, WIDE>::N;
+    const int bx = lanes_for(n, 8), by = kThreads / bx;
+    hipLaunchKernelGGL((k_combine_rows<AT, WIDE>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0, s, ys,
+                       rows, w, resid, T, K, H, bx, out);
+    return hipGetLastError();
+}
+
+template <int AT, bool WIDE>
+hipError_t combine_backward(const void* dout, const void* ys, const int32_t* rows, const float* w, int T, int K, int H,
+                            void* dys, float* dw, hipStream_t s) {
+    const int groups = (K + 7) / 8, per = (K + groups - 1) / groups;
+    hipLaunchKernelGGL((k_combine_rows_backward<AT, WIDE>), dim3((T + kWaves - 1) / kWaves, groups), dim3(kThreads), 0,
+                       s, dout, ys, rows, w, T, K, per, H, dys, dw);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t sort_workspace(int T, int K, int E) {
+    const int64_t P = (int64_t)T * K;
+    if (P <= kOneLaunch) return 0;
+    const int64_t chunk = sort_chunk(P);
+    return (size_t)((P + chunk - 1) / chunk) * (size_t)E * sizeof(int32_t);
+}
+
+hipError_t launch_sort(int atype, const void* x, int64_t stride, const int32_t* ids, int T, int K, int E, int H,
+                       bool f8, void* sorted, float* scales, int32_t* offsets, int32_t* rows, void* workspace,
+                       hipStream_t s) {
+    const Spread a{x, stride, T, K, H, 0, false, sorted, scales};
+    int32_t* counts = static_cast<int32_t*>(workspace);
+    if (atype == A_F32)
+        return f8 ? sort<A_F32, true>(a, ids, E, offsets, rows, counts, s) : sort<A_F32, false>(a, ids, E, offsets, rows, counts, s);
+    return f8 ? sort<A_BF16, true>(a, ids, E, offsets, rows, counts, s) : sort<A_BF16, false>(a, ids, E, offsets, rows, counts, s);
+}
+
+hipError_t launch_combine(int atype, const void* ys, const int32_t* rows, const float* w, const void* resid, int T,
+                          int K, int H, void* out, hipStream_t s) {
+    const int es = atype == A_F32 ? 4 : 2;
+    const bool wide = (int64_t)H * es % 16 == 0 && on16(ys) && on16(out) && (!resid || on16(resid));
+    if (atype == A_F32)
+        return wide ? combine<A_F32, true>(ys, rows, w, resid, T, K, H, out, s) : combine<A_F32, false>(ys, rows, w, resid, T, K, H, out, s);
+    return wide ? combine<A_BF16, true>(ys, rows, w, resid, T, K, H, out, s) : combine<A_BF16, false>(ys, rows, w, resid, T, K, H, out, s);
+}
+
+hipError_t launch_combine_backward(int atype, const void* dout, const void* ys, const int32_t* rows, const float* w,
+                                   int T, int K, int H, void* dys, float* dw, hipStream_t s) {
+    const int es = atype == A_F32 ? 4 : 2;
+    const bool wide = (int64_t)H * es % 16 == 0 && on16(dout) && on16(ys) && on16(dys);
+    if (atype == A_F32)
+        return wide ? combine_backward<A_F32, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
+                    : combine_backward<A_F32, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
+    return wide ? combine_backward<A_BF16, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
+                : combine_backward<A_BF16, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
+}
+
+}  // namespace moe

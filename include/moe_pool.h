@@ -442,6 +442,117 @@ moe_status_t moe_forward_slots(int32_t wtype, int32_t atype, int32_t hidden, int
                                const void* x_dev, const float* topk_w_dev, const void* resid_dev,
                                int32_t n_tokens, void* out_dev, void* stream);
 
+/* ---- the operators around the experts ------------------------------------------ */
+/* A router, tokens sorted by expert and back, and products with 8-bit experts, as calls
+ * of their own: what comes before moe_pool_prepare (its topk_ids and gate weights) and,
+ * for experts that all live in HBM, the layer in four calls: moe_route, moe_sort_tokens
+ * (to e4m3 rows), moe_scaled_product twice, moe_combine_rows.  The router, the sort and
+ * the combine have gradients; the products are a serving format, as the INT4 experts are.
+ *
+ * Every call queues its kernels on `stream` (of the current device, where every buffer
+ * lives) and returns; none allocates, reads back or keeps anything between calls, so
+ * calls on different streams or in captured graphs are independent as long as their
+ * buffers are, and a call with the same inputs gives the same bits.  Buffers are
+ * contiguous but for the row strides (in elements) that are arguments, and do not
+ * overlap.  Sizes: n_tokens * top_k <= 2^24 pairs, top_k <= 64, experts <= 4096, hidden
+ * <= 2^17; n_tokens = 0 is accepted and (but for moe_sort_tokens' offsets) writes nothing. */
+
+/* Top-k of a softmax router ("Running 125B MoE on Two 32 GB Cards", section 4.2: on a
+ * tie of two logits the lower id wins).
+ *  logits_dev    [n_tokens][n_experts] in the activation format, rows logits_stride apart.
+ *  topk_ids_dev  int32 [n_tokens][top_k], written: the largest logits, largest first, equal
+ *                ones in ascending id order.  Always top_k distinct ids in [0, n_experts).
+ *  topk_w_dev    float [n_tokens][top_k], written: MOE_ROUTE_SOFTMAX: the softmax over all
+ *                experts at those ids; MOE_ROUTE_RENORM: the softmax over the chosen alone.
+ * A logit of -inf (an expert masked out) has weight 0 and is chosen only when nothing
+ * else is left; a row of -inf alone gets ids 0 .. top_k - 1 with weights 0.  NaN counts as
+ * -inf.  Logits of +inf share the whole weight equally.  Sums are fp32.
+ * Errors: EINVAL, EHIP. */
+#define MOE_ROUTE_SOFTMAX 0
+#define MOE_ROUTE_RENORM  1
+moe_status_t moe_route(int32_t atype, const void* logits_dev, int64_t logits_stride, int32_t n_tokens,
+                       int32_t n_experts, int32_t top_k, int32_t norm, int32_t* topk_ids_dev, float* topk_w_dev,
+                       void* stream);
+/* Its gradient: from d_topk_w_dev float [n_tokens][top_k] and the call's ids and weights,
+ * d_logits_dev [n_tokens][n_experts] in the activation format, rows d_logits_stride apart
+ * (all n_experts values of a row are written).  With s = sum_k w_k dw_k:
+ *   SOFTMAX: dl_e = p_e (g_e - s), p the softmax over all experts (from logits_dev) and g_e
+ *            the sum of the dw of e;  RENORM: dl_e = the sum over the k of e of w_k (dw_k - s),
+ *            and logits_dev is not read (it may be NULL).
+ * An id outside [0, n_experts) contributes nothing.  Errors: EINVAL, EHIP. */
+moe_status_t moe_route_backward(int32_t atype, const void* logits_dev, int64_t logits_stride,
+                                const int32_t* topk_ids_dev, const float* topk_w_dev, const float* d_topk_w_dev,
+                                int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t norm, void* d_logits_dev,
+                                int64_t d_logits_stride, void* stream);
+
+/* Tokens to one row per (token, k) pair, sorted by expert: the pairs whose id lies in
+ * [0, n_experts), by id and then by (token, k).  Pairs with any other id (padding tokens:
+ * -1) get no row.
+ *  x_dev         [n_tokens][hidden] in the activation format, rows x_stride apart; NULL: the
+ *                places only (hidden, sorted_dev and scales_dev are not looked at).
+ *  sorted_dev    [n_tokens * top_k][hidden], written up to the last pair's row; the rows
+ *                behind it are left as they are.  to_fp8 0: x's rows in its format; to_fp8 1:
+ *                e4m3 codes (hidden a multiple of 16, the buffer on 16 bytes), and
+ *  scales_dev    float [n_tokens * top_k][ceil(hidden / 128)]: per 128 values the smallest
+ *                power of two that brings the largest finite magnitude to 448 or less (at
+ *                least 2^-126; 1 for a block of zeros), each value divided by it and rounded
+ *                to the nearest e4m3 (ties to even).  NaN and infinities become NaN codes.
+ *  offsets_dev   int32 [n_experts + 1], written: the first row of each expert; the last
+ *                entry is the number of rows.
+ *  rows_dev      int32 [n_tokens][top_k], written: the row of each pair, or -1.
+ *  workspace_dev moe_sort_workspace_bytes(n_tokens, top_k, n_experts) bytes on 4 (0: none),
+ *                used by this call only.
+ * The gradient of x is moe_combine_rows of the sorted rows' gradient without weights.
+ * Errors: EINVAL, EHIP. */
+moe_status_t moe_sort_tokens(int32_t atype, const void* x_dev, int64_t x_stride, const int32_t* topk_ids_dev,
+                             int32_t n_tokens, int32_t top_k, int32_t n_experts, int32_t hidden, int32_t to_fp8,
+                             void* sorted_dev, float* scales_dev, int32_t* offsets_dev, int32_t* rows_dev,
+                             void* workspace_dev, size_t workspace_bytes, void* stream);
+/* Bytes of that workspace (0 also for sizes that moe_sort_tokens refuses). */
+size_t moe_sort_workspace_bytes(int32_t n_tokens, int32_t top_k, int32_t n_experts);
+
+/* Sorted rows back to their tokens:
+ *   out[t] = resid[t] + sum_k w[t][k] ys[rows[t][k]]      (fp32, in k order, rounded once)
+ *  ys_dev [n_tokens * top_k][hidden], resid_dev (optional) and out_dev [n_tokens][hidden] in
+ *  the activation format; topk_w_dev float [n_tokens][top_k], or NULL: weights of one.
+ * A place outside [0, n_tokens * top_k) contributes nothing and is not read.
+ * Errors: EINVAL, EHIP. */
+moe_status_t moe_combine_rows(int32_t atype, const void* ys_dev, const int32_t* rows_dev, const float* topk_w_dev,
+                              const void* resid_dev, int32_t n_tokens, int32_t top_k, int32_t hidden, void* out_dev,
+                              void* stream);
+/* Its gradient: d_ys[rows[t][k]] = w[t][k] d_out[t] (rows that no pair has are left as they
+ * are) and d_topk_w[t][k] = <d_out[t], ys[rows[t][k]]> in fp32 (0 for a pair without a row).
+ * The residual's gradient is d_out itself.  The places of rows_dev are distinct, as
+ * moe_sort_tokens gives them.  Errors: EINVAL, EHIP. */
+moe_status_t moe_combine_rows_backward(int32_t atype, const void* d_out_dev, const void* ys_dev,
+                                       const int32_t* rows_dev, const float* topk_w_dev, int32_t n_tokens,
+                                       int32_t top_k, int32_t hidden, void* d_ys_dev, float* d_topk_w_dev,
+                                       void* stream);
+
+/* e4m3 rows times their group's e4m3 matrix, with one scale for each 128 values of a row
+ * and each 128 x 128 values of a matrix; group g has the rows offsets[g] .. offsets[g+1]:
+ *   out[r][n] = sum_b xs[r][b] ws[g][n/128][b] sum_{k in block b} x[r][k] w[g][n][k]
+ * (each block summed in fp32 by the matrix cores, the blocks added in fp32).
+ *  x_dev         e4m3 [n_rows][depth], x_scales_dev float [n_rows][ceil(depth/128)].
+ *  w_dev         e4m3 [n_groups][n_cols][depth], w_scales_dev float
+ *                [n_groups][ceil(n_cols/128)][ceil(depth/128)].  depth: a multiple of 16; x_dev
+ *                and w_dev on 16 bytes.
+ *  offsets_dev   int32 [n_groups + 1], rising within [0, n_rows] (entries that are not count
+ *                as empty groups), or NULL for one group of all n_rows rows.
+ *  epilogue      MOE_PRODUCT_F32 / _BF16: out_dev [n_rows][n_cols] in that format.
+ *                MOE_PRODUCT_SWIGLU (n_cols a multiple of 256): matrix rows [0, n_cols/2) are
+ *                the gate, the rest the up projection; out_dev e4m3 [n_rows][n_cols/2] (on 16
+ *                bytes) and out_scales_dev float [n_rows][n_cols/256]: silu(gate) * up, taken
+ *                in fp32 and rounded as in moe_sort_tokens.
+ * Rows outside every group are left as they are.  Errors: EINVAL, EHIP. */
+#define MOE_PRODUCT_F32    0
+#define MOE_PRODUCT_BF16   1
+#define MOE_PRODUCT_SWIGLU 2
+moe_status_t moe_scaled_product(const void* x_dev, const float* x_scales_dev, const void* w_dev,
+                                const float* w_scales_dev, const int32_t* offsets_dev, int32_t n_rows,
+                                int32_t n_groups, int32_t n_cols, int32_t depth, int32_t epilogue, void* out_dev,
+                                float* out_scales_dev, void* stream);
+
 /* ---- the slot manager alone (host only, no GPU) ----------------------------- */
 /* The same per-layer LRU state machine prepare() runs, driven from host ids, for
  * pool-size planning and for checking the bookkeeping without a GPU.  Semantics

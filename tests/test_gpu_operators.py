@@ -1,0 +1,552 @@
+"""GPU tests of the operators around the experts (router, sorted rows, e4m3 products) against
+oracle/rows.py in float64.
+
+Tolerances come from arithmetic: u = 2^-24 is half a step of fp32, relative to the value; a
+sum of n terms in fp32 is off by at most n u times the sum of their magnitudes, in any
+order; a bf16 output adds half a step, 2^-8 of the value."""
+import numpy as np
+import pytest
+import torch
+
+from _gpu_helpers import DEV
+from expert_slot_cache_amd import binding
+from oracle import rows as orows
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": U, "bf16": 2.0 ** -8}
+F8 = torch.float8_e4m3fn
+
+
+def dev(a, kind=None):
+    t = torch.from_numpy(np.ascontiguousarray(a))
+    return t.to(TYPES[kind] if kind else t.dtype).to(DEV)
+
+
+def host(t):
+    return t.cpu().double().numpy() if t.dtype != F8 else orows.e4m3_widen(t.cpu().view(torch.uint8).numpy())
+
+
+def within(got, ref, bound, what=""):
+    assert got.shape == ref.shape
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), what
+    bad = ~(np.abs(got - ref) <= bound) & ~np.isnan(ref)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, worst {np.nanmax(np.abs(got - ref) - bound):.3e} past"
+
+
+# ---- router --------------------------------------------------------------------------------
+
+INF = float("inf")
+
+
+def logits_for(T, E, seed, special=True):
+    rng = np.random.default_rng(seed)
+    z = (2 * rng.normal(size=(T, E))).astype(np.float32)
+    if special and T >= 8:
+        z[1] = 0.5                                    # all equal
+        z[2] = -INF                                   # masked altogether
+        z[3, ::2] = -INF                              # half masked
+        z[4, E // 2] = np.nan
+        z[5, -1] = INF
+        z[6, :] = -0.0
+        z[6, E // 3] = 0.0                            # both zeros are equal
+        z[7] = np.float32(np.finfo(np.float32).min)   # the lowest value, not -inf
+        z[7, E - 1] = 1.0
+    return z
+
+
+ROUTES = [(1, 1, 1), (1, 64, 8), (9, 7, 7), (8, 5, 4), (130, 60, 6), (65, 128, 8), (33, 200, 10), (9, 512, 10),
+          (8, 1000, 33), (11, 2048, 64), (8, 4096, 64), (8, 4095, 3)]
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,K", ROUTES)
+def test_route(T, E, K, kind, renorm):
+    pad = E + 3 if T % 2 else E                       # rows apart, on no 16 bytes
+    buf = torch.full((T, pad), 9.0, dtype=TYPES[kind], device=DEV)
+    logits = buf[:, :E]
+    logits.copy_(dev(logits_for(T, E, E + K), kind))
+    ids = torch.full((T, K), -7, dtype=torch.int32, device=DEV)
+    w = torch.full((T, K), 9.0, device=DEV)
+    binding.route(logits, ids, w, renorm=renorm)
+    z = host(logits)
+    ref_ids, ref_w = orows.route(z, K, renorm)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    # exp of a difference d: its rounding moves the value by |d| u, the exponential by 2 u
+    # more; E terms are summed and one quotient taken.  Below exp(-88) fp32 has no normal
+    # numbers: 2^-126 absolute.
+    fin = np.where(np.isfinite(z), z, 0)
+    span = np.where(np.abs(fin) < 1e30, np.abs(fin), 0).max() * 2
+    within(host(w), ref_w, ref_w * (2 * span + E + 8) * U + 2.0 ** -126, "weights")
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,K", ROUTES)
+def test_route_backward(T, E, K, kind, renorm):
+    z = logits_for(T, E, 3 * E + K)
+    pad = E + 5 if T % 2 else E
+    lg = torch.full((T, pad), 9.0, dtype=TYPES[kind], device=DEV)[:, :E]
+    lg.copy_(dev(z, kind))
+    z = host(lg)
+    rng = np.random.default_rng(E)
+    ids, w = orows.route(z, K, renorm)
+    if T > 8 and K >= 2:
+        ids[8, 1] = ids[8, 0]                         # the same expert twice
+        ids[0, K - 1] = E                             # and one that is none
+    w, dw = w.astype(np.float32), rng.normal(size=(T, K)).astype(np.float32)
+    buf = torch.full((T, pad), 5.0, dtype=TYPES[kind], device=DEV)
+    out = buf[:, :E]
+    binding.route_backward(None if renorm else lg, dev(ids), dev(w), dev(dw), out, renorm=renorm)
+    assert (buf[:, E:] == 5.0).all()
+    keep = ids < E
+    ref = orows.route_grad(z, np.where(keep, ids, 0), np.where(keep, w, 0), np.where(keep, dw, 0), renorm)
+    # p (g - s): p as in the test of route, s a sum of K products, all relative to
+    # p (|g| + sum |w dw|)
+    fin = np.where(np.isfinite(z), z, 0)
+    span = np.where(np.abs(fin) < 1e30, np.abs(fin), 0).max() * 2
+    size = np.zeros_like(ref)
+    s_abs = (np.abs(w * dw) * keep).sum(1)
+    for t in range(T):
+        p = np.zeros(E)
+        if renorm:
+            np.add.at(p, ids[t][keep[t]], np.abs(w[t][keep[t]]))
+            g = np.abs(dw[t]).max()
+        else:
+            p = orows._terms(np.where(np.isnan(z[t]), -INF, z[t]))
+            p = p / p.sum() if p.sum() > 0 else p
+            g = np.abs(dw[t]).sum()
+        size[t] = p * (g + s_abs[t])
+    within(host(out), ref, size * (2 * span + E + 2 * K + 16) * U + np.abs(ref) * HALF[kind] + 2.0 ** -126, "d_logits")
+
+
+# ---- tokens sorted by expert ---------------------------------------------------------------
+
+def ids_for(T, K, E, seed, holes=0.15):
+    """Distinct ids of a row, some pairs and some whole tokens without an expert."""
+    rng = np.random.default_rng(seed)
+    ids = np.argsort(rng.random((T, E)) + 0.3 * rng.random(E), axis=1)[:, :K].astype(np.int32)
+    if holes:
+        ids[rng.random(T) < holes] = -1
+        ids[rng.random((T, K)) < 0.02] = E
+        ids[rng.random((T, K)) < 0.02] = -(1 << 31)
+    return ids
+
+
+def hidden_for(T, H, seed, kind):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(size=(T, H)).astype(np.float32) * np.exp2(rng.integers(-12, 13, (T, 1))).astype(np.float32)
+    return dev(x, kind)
+
+
+SORTS = [(1, 1, 1, 16), (1, 8, 64, 2048), (8, 8, 64, 144), (128, 8, 60, 48), (129, 8, 64, 256), (700, 3, 5, 1008),
+         (2000, 6, 512, 32), (3, 64, 4096, 16)]
+
+
+@pytest.mark.parametrize("mode", ["bf16", "f32", "bf16->f8", "f32->f8"])
+@pytest.mark.parametrize("T,K,E,H", SORTS)
+def test_sort_tokens(T, K, E, H, mode):
+    kind, f8 = mode.split("->")[0], "f8" in mode
+    if not f8 and T % 2:
+        H += 1                                        # odd rows: one element at a time
+    ids = ids_for(T, K, E, T + K)
+    x = torch.zeros((T, H + 8 * (T % 3)), dtype=TYPES[kind], device=DEV)[:, :H]
+    x.copy_(hidden_for(T, H, T, kind))
+    if T >= 8:
+        x[2] = 0.0
+        x[3, 0] = float("nan")
+        x[4, H - 1] = INF
+        x[5] = 448.0
+        x[6, : H // 2] = 1e-38
+    offsets = torch.full((E + 1,), -5, dtype=torch.int32, device=DEV)
+    rows = torch.full((T, K), -5, dtype=torch.int32, device=DEV)
+    out = torch.full((T * K, H), 3.0, device=DEV).to(F8 if f8 else TYPES[kind])
+    scales = torch.full((T * K, -(-H // 128)), 3.0, device=DEV) if f8 else None
+    binding.sort_tokens(x, dev(ids), out, offsets, rows, scales=scales)
+    ref_off, ref_rows = orows.sort_pairs(ids, E)
+    assert np.array_equal(offsets.cpu().numpy(), ref_off)
+    assert np.array_equal(rows.cpu().numpy(), ref_rows)
+    values, sc = orows.round_rows(host(x)) if f8 else (host(x), None)
+    ref = np.full((T * K, H), 3.0)
+    ref_sc = np.full((T * K, -(-H // 128)), 3.0)
+    for t, k in np.argwhere(ref_rows >= 0):
+        ref[ref_rows[t, k]] = values[t]
+        if f8:
+            ref_sc[ref_rows[t, k]] = sc[t]
+    assert np.array_equal(host(out), ref, equal_nan=True)    # powers of two divide exactly
+    if f8:
+        assert np.array_equal(host(scales), ref_sc)
+
+
+@pytest.mark.parametrize("T,K,E", [(0, 4, 9), (5, 2, 3), (40000, 8, 64), (70000, 4, 4096)])
+def test_sort_places_alone_and_long(T, K, E):
+    """Places without rows to move: no token, none with an expert, and more pairs than 256
+    workgroups take in one pass each."""
+    rng = np.random.default_rng(T)
+    ids = rng.integers(-1, E, (T, K)).astype(np.int32) if T != 5 else np.full((T, K), -1, np.int32)
+    offsets = torch.full((E + 1,), -5, dtype=torch.int32, device=DEV)
+    rows = torch.full((T, K), -5, dtype=torch.int32, device=DEV)
+    need = binding.sort_workspace_bytes(T, K, E)
+    binding.sort_tokens(None, dev(ids), None, offsets, rows,
+                        workspace=torch.empty(need, dtype=torch.uint8, device=DEV) if need else None)
+    flat = ids.reshape(-1)
+    order = np.argsort(np.where(flat < 0, E, flat), kind="stable")
+    order = order[flat[order] >= 0]
+    ref = np.full(T * K, -1, np.int32)
+    ref[order] = np.arange(order.size)
+    assert np.array_equal(rows.cpu().numpy().reshape(-1), ref)
+    assert np.array_equal(offsets.cpu().numpy(), np.searchsorted(flat[order], np.arange(E + 1)))
+
+
+# ---- and back ------------------------------------------------------------------------------
+
+COMBINES = [(1, 1, 1, 8), (1, 8, 64, 2048), (3, 7, 9, 77), (65, 10, 60, 264), (300, 8, 64, 2560), (5, 64, 128, 100),
+            (2, 3, 8, 9000)]
+
+
+@pytest.mark.parametrize("weights,resid", [(True, True), (True, False), (False, False)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,E,H", COMBINES)
+def test_combine_rows(T, K, E, H, kind, weights, resid):
+    rng = np.random.default_rng(T + K)
+    _, rows = orows.sort_pairs(ids_for(T, K, E, H), E)
+    if T >= 3:
+        rows[0, 0], rows[1, K - 1] = T * K, -2        # places of no row
+    ys = hidden_for(T * K, H, K, kind)
+    used = np.zeros(T * K, bool)
+    used[rows[(rows >= 0) & (rows < T * K)]] = True
+    ys[torch.from_numpy(~used).to(DEV)] = float("nan")        # rows of no pair are never read
+    w = dev(rng.random((T, K)).astype(np.float32)) if weights else None
+    res = hidden_for(T, H, 7, kind) if resid else None
+    out = torch.full((T, H), 9.0, dtype=TYPES[kind], device=DEV)
+    binding.combine_rows(ys, dev(rows), out, topk_w=w, resid=res)
+    y, wh, rh = host(ys), host(w) if weights else None, host(res) if resid else None
+    ref = orows.combine(y, rows, wh, rh)
+    size = orows.combine(np.abs(y), rows, wh, np.abs(rh) if resid else None)
+    within(host(out), ref, size * (K + 3) * U + np.abs(ref) * HALF[kind], "out")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,E,H", COMBINES)
+def test_combine_rows_backward(T, K, E, H, kind):
+    rng = np.random.default_rng(T * K)
+    _, rows = orows.sort_pairs(ids_for(T, K, E, H + 1), E)
+    if T >= 3:
+        rows[0, 0], rows[1, K - 1] = T * K, -2
+    ys, d = hidden_for(T * K, H, K, kind), hidden_for(T, H, 9, kind)
+    w = dev(rng.random((T, K)).astype(np.float32))
+    d_ys = torch.full((T * K, H), 9.0, dtype=TYPES[kind], device=DEV)
+    d_w = torch.full((T, K), 9.0, device=DEV)
+    binding.combine_rows_backward(d, ys, dev(rows), w, d_ys, d_w)
+    y, dh, wh = host(ys), host(d), host(w)
+    ref_y, ref_w = orows.combine_grad(dh, y, rows, wh)
+    used = np.zeros(T * K, bool)
+    used[rows[(rows >= 0) & (rows < T * K)]] = True
+    ref_y[~used] = 9.0                                        # left as they were
+    within(host(d_ys), ref_y, np.abs(ref_y) * (HALF[kind] + U), "d_ys")
+    size = orows.combine_grad(np.abs(dh), np.abs(y), rows, wh)[1]
+    within(host(d_w), ref_w, size * (H + 2) * U, "d_w")
+
+
+# ---- e4m3 products -------------------------------------------------------------------------
+
+def codes_for(shape, seed):
+    """e4m3 codes of a normal distribution (none of them NaN)."""
+    rng = np.random.default_rng(seed)
+    v = np.clip(100 * rng.normal(size=shape), -448, 448).astype(np.float32)
+    return torch.from_numpy(v).to(F8)
+
+
+def scales_for(shape, seed):
+    return np.exp2(np.random.default_rng(seed).uniform(-9, -5, shape)).astype(np.float32)
+
+
+def offsets_for(M, G, seed, behind=0):
+    rng = np.random.default_rng(seed)
+    inner = np.sort(rng.integers(0, M - behind + 1, G - 1))
+    return np.concatenate([[0], inner, [M - behind]]).astype(np.int32)
+
+
+class Product:
+    """Inputs of a product, its value in 64 bits and the bound on a kernel's error: a block's
+    128 products are summed by the matrix core (at most two half steps an addition: it may
+    truncate), the blocks and scales in fp32."""
+
+    def __init__(self, M, G, N, K, seed, offsets):
+        nb, kb = -(-N // 128), -(-K // 128)
+        x, w = codes_for((M, K), seed), codes_for((G, N, K), seed + 1)
+        xs, ws = scales_for((M, kb), seed + 2), scales_for((G, nb, kb), seed + 3)
+        self.offsets = offsets
+        self.x, self.xs, self.w, self.ws = x.to(DEV), dev(xs), w.to(DEV), dev(ws)
+        xv = orows.widen_rows(host(x), xs)
+        wv = [orows.widen_matrix(host(w[g]), ws[g]) for g in range(G)]
+        off = offsets if offsets is not None else [0, M]
+        self.ref = orows.scaled_product(xv, wv, off)
+        self.bound = orows.scaled_product(np.abs(xv), [np.abs(v) for v in wv], off) * (256 + 2 * kb + 6) * U
+
+    def call(self, out, **kw):
+        off = None if self.offsets is None else dev(self.offsets)
+        binding.scaled_product(self.x, self.xs, self.w, self.ws, out, offsets=off, **kw)
+
+
+PRODUCTS = [(1, 1, 1, 16), (1, 1, 128, 128), (3, 1, 33, 144), (17, 4, 100, 272), (8, 64, 64, 512), (40, 3, 257, 1040),
+            (200, 5, 384, 256), (333, 2, 130, 640), (700, 3, 512, 384), (1100, 2, 768, 256)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("M,G,N,K", PRODUCTS)
+def test_scaled_product(M, G, N, K, kind):
+    behind = 2 if G > 1 and M > 4 else 0
+    p = Product(M, G, N, K, M + N, offsets_for(M, G, M, behind) if G > 1 else None)
+    out = torch.full((M, N), 7.0, dtype=TYPES[kind], device=DEV)
+    p.call(out)
+    ref = np.where(np.isnan(p.ref), 7.0, p.ref)
+    within(host(out), ref, np.where(np.isnan(p.bound), 0, p.bound) + np.abs(ref) * HALF[kind], "out")
+
+
+@pytest.mark.parametrize("M,G,I,K", [(1, 1, 128, 128), (8, 64, 256, 512), (50, 3, 128, 1040), (300, 2, 384, 256),
+                                     (900, 3, 256, 384)])
+def test_scaled_product_swiglu(M, G, I, K):
+    behind = 1 if G > 1 and M > 4 else 0
+    p = Product(M, G, 2 * I, K, M + I, offsets_for(M, G, M + 1, behind) if G > 1 else None)
+    out = torch.full((M, I), 7.0, device=DEV).to(F8)
+    scales = torch.full((M, I // 128), 7.0, device=DEV)
+    p.call(out, swiglu_scales=scales)
+    got, sc = host(out), host(scales)
+    live = ~np.isnan(p.ref[:, 0])
+    assert (got[~live] == 7.0).all() and (sc[~live] == 7.0).all()
+    got, sc, h, e = got[live], sc[live], p.ref[live], p.bound[live]
+    a = orows.swiglu(h)
+    # |d a| <= 1.1 |up| d gate + |silu| d up, then a few roundings of the value
+    err = 1.1 * np.abs(h[:, I:]) * e[:, :I] + np.abs(h[:, :I]) * e[:, I:] + 1.1 * e[:, :I] * e[:, I:] + 16 * U * np.abs(a)
+    full = np.repeat(sc, 128, axis=1)
+    # half a step of e4m3: 2^-4 of the value, 2^-10 of the scale among the subnormals
+    within(got * full, a, err * (1 + 2.0 ** -4) + np.abs(a) * 2.0 ** -4 + full * 2.0 ** -10, "act")
+    m, _ = np.frexp(sc)
+    assert (m == 0.5).all()                                   # powers of two
+    big = np.abs(a).reshape(len(a), -1, 128).max(2)
+    slack = err.reshape(len(a), -1, 128).max(2)
+    assert (big - slack <= 448 * sc).all() and (big + slack > 224 * sc).all()
+
+
+def test_scaled_product_offsets_that_are_not_rising_stay_inside():
+    """Offsets are device data: falling or outside ones are empty groups, never an access
+    outside the buffers."""
+    M, N, K = 40, 64, 128
+    p = Product(M, 4, N, K, 5, np.array([0, 30, 20, 25, 40], np.int32))
+    out = torch.full((M, N), 7.0, device=DEV)
+    for off in ([0, 30, 20, 25, 40], [-9, -3, 50, 1 << 30, -(1 << 31)], [41, 41, 41, 41, 41]):
+        binding.scaled_product(p.x, p.xs, p.w, p.ws, out, offsets=dev(np.array(off, np.int32)))
+    torch.cuda.synchronize()
+
+
+def test_scaled_product_nan_codes_stay_in_their_row():
+    M, N, K = 20, 48, 256
+    p = Product(M, 1, N, K, 11, None)
+    x = p.x.view(torch.uint8).clone()
+    x[3, 200] = 0x7F
+    out = torch.zeros((M, N), device=DEV)
+    binding.scaled_product(x.view(F8), p.xs, p.w, p.ws, out)
+    nan = torch.isnan(out).cpu().numpy()
+    assert nan[3].all() and not np.delete(nan, 3, axis=0).any()
+
+
+# ---- a run of them together ----------------------------------------------------------------
+
+class Layer:
+    """Router logits -> ids and weights -> sorted e4m3 rows -> both products -> the sum."""
+
+    def __init__(self, T, E, K, H, I, seed):
+        self.T, self.E, self.K, self.H, self.I = T, E, K, H, I
+        rng = np.random.default_rng(seed)
+        self.x = dev(rng.normal(size=(T, H)).astype(np.float32), "bf16")
+        self.logits = dev(rng.normal(size=(T, E)).astype(np.float32), "bf16")
+        self.w13, self.w2 = codes_for((E, 2 * I, H), seed + 1).to(DEV), codes_for((E, H, I), seed + 2).to(DEV)
+        self.s13 = dev(scales_for((E, 2 * I // 128, -(-H // 128)), seed + 3))
+        self.s2 = dev(scales_for((E, -(-H // 128), I // 128), seed + 4))
+        self.buffers()
+
+    def buffers(self):
+        T, E, K, H, I = self.T, self.E, self.K, self.H, self.I
+        self.ids = torch.zeros((T, K), dtype=torch.int32, device=DEV)
+        self.w = torch.zeros((T, K), device=DEV)
+        self.sorted = torch.zeros((T * K, H), device=DEV).to(F8)
+        self.scales = torch.zeros((T * K, -(-H // 128)), device=DEV)
+        self.offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+        self.rows = torch.zeros((T, K), dtype=torch.int32, device=DEV)
+        self.act = torch.zeros((T * K, I), device=DEV).to(F8)
+        self.act_scales = torch.zeros((T * K, I // 128), device=DEV)
+        self.y = torch.zeros((T * K, H), dtype=torch.bfloat16, device=DEV)
+        self.out = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+        self.ws = torch.zeros(max(1, binding.sort_workspace_bytes(T, K, E)), dtype=torch.uint8, device=DEV)
+
+    def run(self):
+        binding.route(self.logits, self.ids, self.w)
+        binding.sort_tokens(self.x, self.ids, self.sorted, self.offsets, self.rows, scales=self.scales, workspace=self.ws)
+        binding.scaled_product(self.sorted, self.scales, self.w13, self.s13, self.act, offsets=self.offsets,
+                               swiglu_scales=self.act_scales)
+        binding.scaled_product(self.act, self.act_scales, self.w2, self.s2, self.y, offsets=self.offsets)
+        binding.combine_rows(self.y, self.rows, self.out, topk_w=self.w, resid=self.x)
+        return self.out
+
+    def reference(self):
+        x = host(self.x)
+        ids, w = orows.route(host(self.logits), self.K, True)
+        v, sc = orows.round_rows(x)
+        xq = orows.widen_rows(v, sc)
+        out, size = x.copy(), np.abs(x)
+        mats = {}
+        for t in range(self.T):
+            for k in range(self.K):
+                e = int(ids[t, k])
+                if e not in mats:
+                    mats[e] = (orows.widen_matrix(host(self.w13[e]), self.s13[e].cpu().numpy()),
+                               orows.widen_matrix(host(self.w2[e]), self.s2[e].cpu().numpy()))
+                a, s = orows.round_rows(orows.swiglu((mats[e][0] @ xq[t])[None]))
+                a = orows.widen_rows(a, s)[0]
+                out[t] += w[t, k] * (mats[e][1] @ a)
+                size[t] += w[t, k] * (np.abs(mats[e][1]) @ np.abs(a))
+        return out, size
+
+
+@pytest.mark.parametrize("T,E,K,H,I", [(1, 16, 4, 256, 128), (6, 8, 2, 272, 256), (150, 8, 4, 256, 256)])
+def test_layer_of_operators(T, E, K, H, I):
+    layer = Layer(T, E, K, H, I, 3)
+    got = host(layer.run())
+    ref, size = layer.reference()
+    # the rows y and the sum are rounded to bf16 (2^-8 each).  An activation next to the border
+    # of two e4m3 codes may fall to the other side, a step of at most 2^-3 of itself; fp32 puts
+    # one in some 10^4 there, so at most one of the I in a row's sum: 2^-3 of its share, and no
+    # share of these sums is over 8 / I of the whole.
+    within(got, ref, size * (2 * 2.0 ** -8 + 2.0 ** -3 * 8 / I), "out")
+
+
+def test_layer_replayed_from_a_graph_and_on_another_stream():
+    """The captured layer gives the eager bits on every replay, with eager work in between,
+    new inputs and a second layer captured beside it."""
+    a, b = Layer(150, 8, 4, 256, 256, 3), Layer(5, 8, 4, 256, 128, 4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a.run()
+        b.run()
+    torch.cuda.synchronize()
+    graphs = []
+    for layer in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            layer.run()
+        graphs.append(g)
+    for seed in range(4):
+        rng = np.random.default_rng(seed)
+        for layer, g in zip((a, b), graphs):
+            layer.x.copy_(dev(rng.normal(size=(layer.T, layer.H)).astype(np.float32), "bf16"))
+            layer.logits.copy_(dev(rng.normal(size=(layer.T, layer.E)).astype(np.float32), "bf16"))
+            eager = layer.run().clone()
+            layer.out.zero_()
+            layer.act.view(torch.uint8).zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(layer.out, eager)
+            with torch.cuda.stream(side):
+                layer.out.zero_()
+                layer.run()
+            side.synchronize()
+            assert torch.equal(layer.out, eager)
+
+
+@pytest.mark.parametrize("T,K,E,H", [(20, 3, 8, 40), (300, 4, 8, 64)])
+def test_gradient_through_sort_and_combine(T, K, E, H):
+    """Rows to experts and back around a per-expert linear map, in fp32: the gradients of the
+    tokens and of the weights against differences.  The map is linear in both, so a difference
+    of any size is exact but for rounding: (sums of H + K terms) u of the magnitudes."""
+    rng = np.random.default_rng(T)
+    ids = ids_for(T, K, E, 5)
+    idd = dev(ids)
+    gain = dev(rng.normal(size=(E, H)).astype(np.float32))
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    rows = torch.zeros((T, K), dtype=torch.int32, device=DEV)
+    xs = torch.zeros((T * K, H), device=DEV)
+
+    def forward(x, w):
+        binding.sort_tokens(x, idd, xs, offsets, rows)
+        n = int(offsets[-1])
+        which = torch.searchsorted(offsets[1:].contiguous(), torch.arange(n, device=DEV, dtype=torch.int32), right=True)
+        ys = torch.zeros_like(xs)
+        ys[:n] = xs[:n] * gain[which]
+        out = torch.zeros((T, H), device=DEV)
+        binding.combine_rows(ys, rows, out, topk_w=w)
+        return out, ys, which, n
+
+    x, w = dev(rng.normal(size=(T, H)).astype(np.float32)), dev(rng.random((T, K)).astype(np.float32))
+    d = dev(rng.normal(size=(T, H)).astype(np.float32))
+    out, ys, which, n = forward(x, w)
+    d_ys, d_w = torch.zeros_like(ys), torch.zeros_like(w)
+    binding.combine_rows_backward(d, ys, rows, w, d_ys, d_w)
+    d_xs = torch.zeros_like(ys)
+    d_xs[:n] = d_ys[:n] * gain[which]
+    d_x = torch.zeros_like(x)
+    binding.combine_rows(d_xs, rows, d_x)
+    vx, vw = torch.randn_like(x), torch.randn_like(w)
+    for moved, grad, v in ((forward(x + vx, w)[0], d_x, vx), (forward(x, w + vw)[0], d_w, vw)):
+        got = ((moved - out).double() * d.double()).sum().item()
+        want = (grad.double() * v.double()).sum().item()
+        size = (d.abs().double() * (moved.abs() + out.abs() + K * 16).double()).sum().item()
+        assert abs(got - want) <= size * (H + K + 8) * U
+
+
+# ---- refusals of the binding ---------------------------------------------------------------
+
+def test_binding_refuses_what_does_not_fit():
+    f32 = lambda *s: torch.zeros(s, device=DEV)                      # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)   # noqa: E731
+    f8 = lambda *s: f32(*s).to(F8)                                   # noqa: E731
+    calls = [
+        lambda: binding.route(f32(4, 8).cpu(), i32(4, 2), f32(4, 2)),
+        lambda: binding.route(f32(4, 8).half(), i32(4, 2), f32(4, 2)),
+        lambda: binding.route(f32(8, 4).t(), i32(4, 2), f32(4, 2)),
+        lambda: binding.route(f32(1, 8).expand(4, 8), i32(4, 2), f32(4, 2)),
+        lambda: binding.route(f32(4, 8), i32(4, 2).long(), f32(4, 2)),
+        lambda: binding.route(f32(4, 8), i32(4, 2), f32(4, 3)),
+        lambda: binding.route(f32(4, 8), i32(4, 9), f32(4, 9)),
+        lambda: binding.route(f32(32), i32(4, 2), f32(4, 2)),
+        lambda: binding.route_backward(None, i32(4, 2), f32(4, 2), f32(4, 2), f32(4, 8), renorm=False),
+        lambda: binding.route_backward(f32(4, 8).bfloat16(), i32(4, 2), f32(4, 2), f32(4, 2), f32(4, 8)),
+        lambda: binding.sort_tokens(f32(4, 24), i32(4, 2), f8(8, 24), i32(9), i32(4, 2), scales=f32(8, 1)),
+        lambda: binding.sort_tokens(f32(4, 16), i32(4, 2), f32(7, 16), i32(9), i32(4, 2)),
+        lambda: binding.sort_tokens(f32(4, 16), i32(4, 2), f32(8, 16), i32(1), i32(4, 2)),
+        lambda: binding.sort_tokens(None, i32(4000, 2), None, i32(9), i32(4000, 2),
+                                    workspace=torch.zeros(8, dtype=torch.uint8, device=DEV)),
+        lambda: binding.sort_tokens(None, i32(4000, 2), None, i32(9), i32(4000, 2),
+                                    stream=torch.cuda.Stream().cuda_stream),
+        lambda: binding.combine_rows(f32(8, 16), i32(4, 2), f32(4, 16).bfloat16()),
+        lambda: binding.combine_rows(f32(8, 16), i32(4, 2), f32(4, 16), resid=f32(4, 8)),
+        lambda: binding.combine_rows_backward(f32(4, 16), f32(8, 16), i32(4, 2), f32(4, 2), f32(8, 15), f32(4, 2)),
+        lambda: binding.scaled_product(f8(4, 24), f32(4, 1), f8(1, 8, 24), f32(1, 1, 1), f32(4, 8)),
+        lambda: binding.scaled_product(f8(4, 32), f32(4, 1), f8(2, 8, 32), f32(2, 1, 1), f32(4, 8)),
+        lambda: binding.scaled_product(f8(4, 32), f32(4, 2), f8(1, 8, 32), f32(1, 1, 1), f32(4, 8)),
+        lambda: binding.scaled_product(f8(4, 32), f32(4, 1), f8(1, 128, 32), f32(1, 1, 1), f8(4, 64),
+                                       swiglu_scales=f32(4, 0)),
+        lambda: binding.scaled_product(f8(4, 32)[:, 16:], f32(4, 1), f8(1, 8, 16), f32(1, 1, 1), f32(4, 8)),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(binding.MoeError) as e:
+            call()
+        assert e.value.status == binding.EINVAL, i
+
+
+def test_no_tokens():
+    z = lambda *s: torch.zeros(s, device=DEV)                        # noqa: E731
+    i = lambda *s: torch.full(s, 5, dtype=torch.int32, device=DEV)   # noqa: E731
+    off = i(9)
+    binding.route(z(0, 8), i(0, 2), z(0, 2))
+    binding.route_backward(z(0, 8), i(0, 2), z(0, 2), z(0, 2), z(0, 8))
+    binding.sort_tokens(z(0, 16), i(0, 2), z(0, 16), off, i(0, 2))
+    binding.combine_rows(z(0, 16), i(0, 2), z(0, 16))
+    binding.combine_rows_backward(z(0, 16), z(0, 16), i(0, 2), z(0, 2), z(0, 16), z(0, 2))
+    binding.scaled_product(z(0, 16).to(F8), z(0, 1), z(8, 4, 16).to(F8), z(8, 1, 1), z(0, 4), offsets=off)
+    assert (off == 0).all()
