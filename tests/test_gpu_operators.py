@@ -270,10 +270,19 @@ def offsets_for(M, G, seed, behind=0):
     return np.concatenate([[0], inner, [M - behind]]).astype(np.int32)
 
 
+def eights(v):
+    """The largest magnitude of each eight values of a row (padded to whole ones)."""
+    v = np.pad(np.abs(v), ((0, 0), (0, -v.shape[1] % 8)))
+    return v.reshape(v.shape[0], -1, 8).max(2)
+
+
 class Product:
-    """Inputs of a product, its value in 64 bits and the bound on a kernel's error: a block's
-    128 products are summed by the matrix core (at most two half steps an addition: it may
-    truncate), the blocks and scales in fp32."""
+    """Inputs of a product, its value in 64 bits and bounds on a kernel's error.  `bound`, for
+    fp32 outputs: a block's 128 products are summed by the matrix core (at most two half steps
+    an addition: it may truncate), the blocks and scales in fp32.  `coarse`, for the bf16 and
+    e4m3 outputs: the fp8 matrix instruction drops what lies 13 bits below the largest of each
+    eight products, less than 8 * 2^-13 of that largest an eight, and the largest product of an
+    eight is at most the product of the largest factors."""
 
     def __init__(self, M, G, N, K, seed, offsets):
         nb, kb = -(-N // 128), -(-K // 128)
@@ -286,6 +295,7 @@ class Product:
         off = offsets if offsets is not None else [0, M]
         self.ref = orows.scaled_product(xv, wv, off)
         self.bound = orows.scaled_product(np.abs(xv), [np.abs(v) for v in wv], off) * (256 + 2 * kb + 6) * U
+        self.coarse = self.bound + orows.scaled_product(eights(xv), [eights(v) for v in wv], off) * 2.0 ** -10
 
     def call(self, out, **kw):
         off = None if self.offsets is None else dev(self.offsets)
@@ -293,7 +303,8 @@ class Product:
 
 
 PRODUCTS = [(1, 1, 1, 16), (1, 1, 128, 128), (3, 1, 33, 144), (17, 4, 100, 272), (8, 64, 64, 512), (40, 3, 257, 1040),
-            (200, 5, 384, 256), (333, 2, 130, 640), (700, 3, 512, 384), (1100, 2, 768, 256)]
+            (200, 5, 384, 256), (333, 2, 130, 640), (700, 3, 512, 384), (1100, 2, 768, 256), (90, 1, 257, 1040),
+            (50, 3, 300, 1040), (600, 2, 520, 272), (150, 2, 1000, 16), (260, 1, 24, 128), (2049, 8, 264, 400)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -304,10 +315,12 @@ def test_scaled_product(M, G, N, K, kind):
     out = torch.full((M, N), 7.0, dtype=TYPES[kind], device=DEV)
     p.call(out)
     ref = np.where(np.isnan(p.ref), 7.0, p.ref)
-    within(host(out), ref, np.where(np.isnan(p.bound), 0, p.bound) + np.abs(ref) * HALF[kind], "out")
+    bound = p.bound if kind == "f32" else p.coarse
+    within(host(out), ref, np.where(np.isnan(bound), 0, bound) * (1 + HALF[kind]) + np.abs(ref) * HALF[kind], "out")
 
 
 @pytest.mark.parametrize("M,G,I,K", [(1, 1, 128, 128), (8, 64, 256, 512), (50, 3, 128, 1040), (300, 2, 384, 256),
+                                     (180, 2, 256, 144), (70, 1, 128, 640), (1500, 4, 128, 272),
                                      (900, 3, 256, 384)])
 def test_scaled_product_swiglu(M, G, I, K):
     behind = 1 if G > 1 and M > 4 else 0
@@ -318,7 +331,7 @@ def test_scaled_product_swiglu(M, G, I, K):
     got, sc = host(out), host(scales)
     live = ~np.isnan(p.ref[:, 0])
     assert (got[~live] == 7.0).all() and (sc[~live] == 7.0).all()
-    got, sc, h, e = got[live], sc[live], p.ref[live], p.bound[live]
+    got, sc, h, e = got[live], sc[live], p.ref[live], p.coarse[live]
     a = orows.swiglu(h)
     # |d a| <= 1.1 |up| d gate + |silu| d up, then a few roundings of the value
     err = 1.1 * np.abs(h[:, I:]) * e[:, :I] + np.abs(h[:, :I]) * e[:, I:] + 1.1 * e[:, :I] * e[:, I:] + 16 * U * np.abs(a)
