@@ -57,7 +57,7 @@ struct Tile {
 template <int TM>
 struct Tiles {
     const int32_t* offsets;
-    int M, g0, g1, own, incl, total;
+    int M, g0, g1, lo0, hi0, own, incl, total;   // lo0, hi0: the rows of group g0
     __device__ __forceinline__ Tiles(const int32_t* __restrict__ off, int G, int M_) : offsets(off), M(M_) {
         if (!off) {
             total = (M + TM - 1) / TM;
@@ -67,9 +67,11 @@ struct Tiles {
         const int per = (G + 63) >> 6;
         g0 = min(lane * per, G);
         g1 = min(g0 + per, G);
-        own = 0;
-        int lo = bound(off[g0], 0);
-        for (int g = g0; g < g1; ++g) {
+        lo0 = bound(off[g0], 0);
+        hi0 = g0 < g1 ? bound(off[g0 + 1], lo0) : lo0;
+        own = (hi0 - lo0 + TM - 1) / TM;
+        int lo = hi0;
+        for (int g = g0 + 1; g < g1; ++g) {
             const int hi = bound(off[g + 1], lo);
             own += (hi - lo + TM - 1) / TM;
             lo = hi;
@@ -90,9 +92,9 @@ struct Tiles {
         int group = 0, row0 = 0, rows = 0;
         if ((int)(threadIdx.x & 63) == who) {
             int left = tile - (incl - own);
-            int lo = bound(offsets[g0], 0);
+            int lo = lo0;
             for (int g = g0; g < g1; ++g) {
-                const int hi = bound(offsets[g + 1], lo);
+                const int hi = g == g0 ? hi0 : bound(offsets[g + 1], lo);
                 const int n = (hi - lo + TM - 1) / TM;
                 if (left < n) {
                     group = g;
@@ -111,156 +113,18 @@ struct Tiles {
 
 __device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
 
-// Few rows per group: the matrix streams from memory straight into MFMA operands.
-// A workgroup takes MT tiles of 16 rows of one group and 16 NT WN matrix rows; its WN x KS
-// waves split the matrix rows and the blocks of k (wave ks takes blocks ks, ks + KS, ...),
-// and the KS partial sums meet in LDS, in order.  SwiGLU: WN = 8, NT = 2, a wave's two tiles
-// being 16 gate rows and the 16 up rows of the same columns, so that a workgroup holds all
-// 128 columns that share a scale.
-template <int NT, int MT, int WN, int KS, int OUT>
-__global__ __launch_bounds__(64 * WN * KS) void k_product_stream(ProductArgs a, int nblocks, int kb_n) {
-    constexpr int U = WN * KS >= 16 ? 2 : 4;          // blocks of k requested at a time
-    constexpr int COLS = OUT == OUT_SWIGLU ? 16 * WN : 16 * NT * WN;   // columns written
-    constexpr int PAD = 4;                            // floats: column runs start on other banks
-    __shared__ float red[KS][NT][MT][WN][16][16 + PAD];
-    const int nb = blockIdx.x % nblocks, tile = blockIdx.x / nblocks;
-    const Tiles<16 * MT> tiles(a.offsets, a.G, a.M);
-    if (tile >= tiles.total) return;
-    const Tile tl = tiles.at(tile);
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wn = wave % WN, ks = wave / WN;
-    const int q = lane >> 4, l16 = lane & 15;
-    const int K = a.K;
-    const int n_half = a.N / 2;
-    const uint8_t* wg = a.w + (size_t)tl.group * a.N * K;
-    const float* sg = a.ws + (size_t)tl.group * ((a.N + kBlock - 1) / kBlock) * kb_n;
-    const uint8_t* wp[NT];
-    const float* sp[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        int n0 = OUT == OUT_SWIGLU ? t * n_half + nb * COLS + wn * 16 : nb * COLS + (wn * NT + t) * 16;
-        n0 = min(n0, a.N - 1);
-        sp[t] = sg + (size_t)(n0 / kBlock) * kb_n;
-        wp[t] = wg + (size_t)min(n0 + l16, a.N - 1) * K;
-    }
-    const uint8_t* xp[MT];
-    const float* xsp[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const size_t r = tl.row0 + min(m * 16 + l16, tl.rows - 1);   // rows past the end: never stored
-        xp[m] = a.x + r * K;
-        xsp[m] = a.xs + r * kb_n;
-    }
-    f32x4_t acc[NT][MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    for (int kb0 = ks; kb0 < kb_n; kb0 += KS * U) {
-        uint4 wv[U][NT][2], xv[U][MT][2];
-        float ss[U][NT], xs[U][MT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kb = kb0 + u * KS;
-            const int k = kb * kBlock + q * 16;
-            const bool in0 = k < K, in1 = k + 64 < K;   // K is a multiple of 16
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                wv[u][t][0] = in0 ? *reinterpret_cast<const uint4*>(wp[t] + k) : none;
-                wv[u][t][1] = in1 ? *reinterpret_cast<const uint4*>(wp[t] + k + 64) : none;
-                ss[u][t] = kb < kb_n ? sp[t][kb] : 0.0f;
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                xv[u][m][0] = in0 ? *reinterpret_cast<const uint4*>(xp[m] + k) : none;
-                xv[u][m][1] = in1 ? *reinterpret_cast<const uint4*>(xp[m] + k + 64) : none;
-                xs[u][m] = kb < kb_n ? xsp[m][kb] : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (kb0 + u * KS < kb_n) {
-                Wide xw[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) xw[m] = widen_block(xv[u][m]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const Wide ww = widen_block(wv[u][t]);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const f32x4_t part = mfma_block(ww, xw[m]);
-                        const float s = ss[u][t] * xs[u][m];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[t][m][i] += s * part[i];
-                    }
-                }
-            }
-    }
-    // accumulator element i: matrix row 4 (lane/16) + i of the tile, token lane % 16
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-            *reinterpret_cast<f32x4_t*>(&red[ks][t][m][wn][l16][4 * q]) = acc[t][m];
-    __syncthreads();
-    if constexpr (OUT == OUT_SWIGLU) {
-        // 32 lanes a row, 4 columns each
-        for (int it = threadIdx.x; it < MT * 16 * 32; it += 64 * WN * KS) {
-            const int c4 = it & 31, r = it >> 5;
-            const int m = r >> 4, l = r & 15, wc = c4 >> 2, c = (c4 & 3) * 4;
-            float v[4], big = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float g = 0.0f, u = 0.0f;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    g += red[s][0][m][wc][l][c + i];
-                    u += red[s][NT - 1][m][wc][l][c + i];
-                }
-                v[i] = silu_mul(g, u);
-                const float mag = fabsf(v[i]);
-                if (mag < __builtin_inff()) big = fmaxf(big, mag);
-                else v[i] = __builtin_nanf("");
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) big = fmaxf(big, __shfl_xor(big, d));
-            if (r < tl.rows) {
-                const float scale = f8_scale(big), inv = f8_inverse(scale);
-                const size_t row = tl.row0 + r;
-                *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + row * n_half + nb * COLS + c4 * 4) =
-                    f8_pack(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-                if (c4 == 0) a.os[row * (n_half / kBlock) + nb] = scale;
-            }
-        }
-    } else {
-        for (int it = threadIdx.x; it < MT * 16 * COLS; it += 64 * WN * KS) {
-            const int c = it % COLS, r = it / COLS;
-            const int n = nb * COLS + c;
-            if (r >= tl.rows || n >= a.N) continue;
-            const int wc = c / (16 * NT), t = (c / 16) % NT;
-            float v = 0.0f;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) v += red[s][t][r >> 4][wc][r & 15][c & 15];
-            store_one<OUT == OUT_F32 ? A_F32 : A_BF16>(a.out, (size_t)(tl.row0 + r) * a.N + n, v);
-        }
-    }
-}
-
-// ---- many rows per group: tiles staged through LDS -----------------------------------------
+// ---- the kernel ------------------------------------------------------------------------------
 //
-// A workgroup of eight waves takes 256 matrix rows x TT rows of one group.  A stage is one
-// block of 128: 128 bytes of each matrix row and token row, copied from memory straight into
-// LDS (16 bytes a lane, no registers), and the block's scales; S stages form a ring, filled
-// S - 1 stages ahead, with one barrier per stage.  In LDS a row is eight 16-byte chunks, chunk
-// c at place c ^ (row % 8), so that the sixteen rows a fragment reads at one chunk lie in
-// different banks; the copy places lane i's 16 bytes at 16 i, so a lane picks its source
-// chunk accordingly.
+// A workgroup takes TW matrix rows x TT rows of one group.  A stage is one block of 128: 128
+// bytes of each matrix row and token row, copied from memory straight into LDS (16 bytes a
+// lane, no registers), and the block's scales; S stages form a ring, filled S - 1 stages
+// ahead, with one barrier per stage.  In LDS a row is eight 16-byte chunks, chunk c at place
+// c ^ (row % 8), so that the rows a fragment reads at one chunk lie in different banks; the
+// copy places lane i's 16 bytes at 16 i, so a lane picks its source chunk accordingly.
 //
-// The waves form WW x WT; each computes 16 FA matrix rows x 64 token rows.  The matrix rows
-// of a wave are dealt to its FA fragments four at a time, so that the fragments' accumulators
-// of one lane are consecutive columns of the output, stored 16 bytes at a time.
+// The waves form WW x WT; each computes 16 FA matrix rows x 16 FB token rows.  The matrix
+// rows of a wave are dealt to its FA fragments four at a time, so that the fragments'
+// accumulators of one lane are consecutive columns of the output.
 //
 // The bf16 and e4m3 outputs use the fp8 matrix instruction (twice the bf16 rate).  It aligns
 // each eight products (k .. k+7) to the largest of them and keeps 13 bits below its leading
@@ -277,15 +141,16 @@ __device__ __forceinline__ f32x4_t mfma_codes(const uint4 a[2], const uint4 b[2]
 }
 
 // 16 (or 4) bytes per lane from memory to LDS: lane i's go to lds + 16 i (4 i).  The compiler
-// does not count these loads: the kernel waits for them itself, before its barrier.
+// does not count these loads: the kernel waits for them itself, before its barrier.  M0 holds
+// the LDS address; the compiler keeps nothing there (it sets it right before its own uses).
 __device__ __forceinline__ void copy16(uint32_t lds, uint32_t voff, const uint8_t* base) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t lds, const uint8_t* p) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const float* p) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 // All but this wave's newest N copies have landed and its LDS reads are done, and so for
 // every wave of the workgroup.
@@ -296,27 +161,30 @@ __device__ __forceinline__ void wait_and_meet() {
 
 __device__ __align__(16) const uint8_t k_zeros[16] = {};   // what lies past the end of a row
 
-template <int TT, int OUT>
-struct TileShape {
-    static constexpr int TW = 256;
-    static constexpr int WT = TT / 64, WW = 8 / WT;       // waves along tokens, along matrix rows
-    static constexpr int FA = TW / WW / 16, FB = 4;       // fragments of a wave
-    static constexpr int NA = TW / 64, NB = TT / 64;      // copies per wave and stage (8 rows each)
-    static constexpr int SCALES = (TW + TT) * 128;        // offset of a stage's scales: TT, then the matrix'
-    static constexpr int STAGE = SCALES + 8 * 64 * 4;
-    static constexpr int S = TT == 256 ? 2 : 3;
-    static constexpr int COPIES = NA + NB + 1;
+template <int TW_, int TT_, int WAVES_, int S_>
+struct Shape {
+    static constexpr int TW = TW_, TT = TT_, WAVES = WAVES_, S = S_;
+    static constexpr int WT = TT > 64 ? TT / 64 : 1;       // waves along tokens,
+    static constexpr int WW = WAVES / WT;                  // along matrix rows
+    static constexpr int FA = TW / WW / 16, FB = TT / WT / 16;   // fragments of a wave
+    static constexpr int NA = TW / 8 / WAVES;              // a wave's copies of 8 matrix rows,
+    static constexpr int NB = TT / 8 / WAVES;              // of 8 token rows (0: not every wave has one)
+    static constexpr int XWAVES = TT / 8;                  // waves with one, where NB is 0
+    static constexpr int SWAVES = (TT + 2 + 63) / 64;      // the last waves copy the scales, 64 each
+    static constexpr int SCALES = (TW + TT) * 128;         // their place in a stage: TT, then the matrix'
+    static constexpr int STAGE = SCALES + SWAVES * 256;
     static constexpr int LDS = S * STAGE;
-    static constexpr int COLS = OUT == OUT_SWIGLU ? TW / 2 : TW;
+    static_assert(FA >= 1 && FB >= 1 && NA >= 1 && (NB > 0 || XWAVES + SWAVES <= WAVES) && SWAVES <= WAVES, "");
 };
 
-template <int TT, int OUT>
-__global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblocks, int kb_n) {
-    using C = TileShape<TT, OUT>;
+template <class C, int OUT>
+__global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nblocks, int kb_n) {
     constexpr bool GATED = OUT == OUT_SWIGLU;
-    constexpr int FA = C::FA, FB = C::FB, NA = C::NA, NB = C::NB;
+    constexpr int FA = C::FA, FB = C::FB, NA = C::NA, NB = C::NB, TT = C::TT, WAVES = C::WAVES;
     constexpr int HF = GATED ? FA / 2 : FA;               // fragments of one half
     constexpr int CF = HF < 4 ? HF : 4;                   // fragments that share runs of columns
+    constexpr int COLS = GATED ? C::TW / 2 : C::TW;       // columns written
+    static_assert(!GATED || (C::TW == 256 && HF >= 1), "a scale's 128 columns in one workgroup");
     __shared__ __align__(1024) char lds[C::LDS];
     const Tiles<TT> tiles(a.offsets, a.G, a.M);
     // workgroup b runs on XCD b % 8: each XCD takes one contiguous run of the (tile, column
@@ -337,31 +205,36 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
     const uint8_t* wg = a.w + (size_t)tl.group * a.N * K;
     const float* sg = a.ws + (size_t)tl.group * ((a.N + kBlock - 1) / kBlock) * kb_n;
 
-    // this wave's copies: LDS rows (wave + 8 i) * 8 + lane / 8
+    // this wave's copies: LDS rows (wave + WAVES i) * 8 + lane / 8
     const int l8 = lane >> 3, chunk = ((lane & 7) ^ l8) * 16;
-    uint32_t aoff[NA], boff[NB];
+    constexpr int NB1 = NB > 0 ? NB : 1;
+    uint32_t aoff[NA], boff[NB1];
     const uint8_t* abase[NA];
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
-        const int row = (wave + 8 * i) * 8;               // of this copy's first LDS row
+        const int row = (wave + WAVES * i) * 8;           // of this copy's first LDS row
         const int sec = row / (16 * FA), j = (row / 16) % FA, r = (row % 16) + l8;
         const int half = GATED ? j / HF : 0, jj = GATED ? j % HF : j;
         const int col = sec * 16 * HF + (jj / CF) * 16 * CF + (r >> 2) * 4 * CF + (jj % CF) * 4 + (r & 3);
-        const int n0 = half * n_half + nb * C::COLS;
+        const int n0 = half * n_half + nb * COLS;
         abase[i] = wg + (size_t)n0 * K;
         aoff[i] = (uint32_t)min(col, a.N - 1 - n0) * (uint32_t)K + chunk;   // rows past the end: never stored
     }
+    const bool has_x = NB > 0 || wave < C::XWAVES;
     const uint8_t* bbase = a.x + (size_t)tl.row0 * K;
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-        boff[i] = (uint32_t)min((wave + 8 * i) * 8 + l8, tl.rows - 1) * (uint32_t)K + chunk;
-    // the scales: slot wave * 64 + lane holds a token's, the slots behind them the matrix'
-    const int slot = wave * 64 + lane;
-    // the matrix' blocks of 128 rows: gate and up, or the two of these 256 rows
+    for (int i = 0; i < NB1; ++i)
+        boff[i] = (uint32_t)min((wave + WAVES * i) * 8 + l8, tl.rows - 1) * (uint32_t)K + chunk;
+    // the scales: slot i < TT holds token i's, the slots behind them those of the matrix' blocks
+    // of 128 rows: gate and up, or the one or two of these TW rows
+    const bool has_s = wave >= WAVES - C::SWAVES;
+    const int slot = (wave - (WAVES - C::SWAVES)) * 64 + lane;
     const int nb_last = (a.N + kBlock - 1) / kBlock - 1;
-    const int second = GATED ? n_half / kBlock + nb : min(2 * nb + 1, nb_last);
-    const float* sp = slot < TT ? a.xs + (size_t)(tl.row0 + min(slot, tl.rows - 1)) * kb_n
-                                : sg + (size_t)(slot == TT + 1 ? second : GATED ? nb : 2 * nb) * kb_n;
+    const int first = GATED ? nb : nb * COLS / kBlock;
+    const int second = GATED ? n_half / kBlock + nb : min(first + 1, nb_last);
+    const float* sp = slot < TT ? a.xs + (size_t)(tl.row0 + min(max(slot, 0), tl.rows - 1)) * kb_n
+                                : sg + (size_t)(slot == TT + 1 ? second : first) * kb_n;
+    const int copies = NA + (NB > 0 ? NB : has_x ? 1 : 0) + (has_s ? 1 : 0);   // of this wave, a stage
     const bool tail = K % kBlock != 0;
 
     auto fill = [&](int kb, int stage) {
@@ -370,16 +243,19 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
         if (tail && kb == kb_n - 1) {
             const bool in = (int)k0 + chunk < K;
 #pragma unroll
-            for (int i = 0; i < NA; ++i) copy16(at + (wave + 8 * i) * 1024, in ? abase[i] + aoff[i] + k0 : k_zeros);
+            for (int i = 0; i < NA; ++i) copy16(at + (wave + WAVES * i) * 1024, in ? abase[i] + aoff[i] + k0 : k_zeros);
+            if (has_x)
 #pragma unroll
-            for (int i = 0; i < NB; ++i) copy16(at + C::TW * 128 + (wave + 8 * i) * 1024, in ? bbase + boff[i] + k0 : k_zeros);
+                for (int i = 0; i < NB1; ++i)
+                    copy16(at + C::TW * 128 + (wave + WAVES * i) * 1024, in ? bbase + boff[i] + k0 : k_zeros);
         } else {
 #pragma unroll
-            for (int i = 0; i < NA; ++i) copy16(at + (wave + 8 * i) * 1024, aoff[i], abase[i] + k0);
+            for (int i = 0; i < NA; ++i) copy16(at + (wave + WAVES * i) * 1024, aoff[i], abase[i] + k0);
+            if (has_x)
 #pragma unroll
-            for (int i = 0; i < NB; ++i) copy16(at + C::TW * 128 + (wave + 8 * i) * 1024, boff[i], bbase + k0);
+                for (int i = 0; i < NB1; ++i) copy16(at + C::TW * 128 + (wave + WAVES * i) * 1024, boff[i], bbase + k0);
         }
-        copy4(at + C::SCALES + wave * 256, sp + kb);
+        if (has_s) copy4(at + C::SCALES + (wave - (WAVES - C::SWAVES)) * 256, sp + kb);
     };
 
     f32x4_t acc[FA][FB];
@@ -387,66 +263,69 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
     for (int j = 0; j < FA; ++j)
 #pragma unroll
         for (int m = 0; m < FB; ++m) acc[j][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const bool idle = wt * 64 >= tl.rows;                  // no token of this wave: it only copies
+    const bool idle = wt * 16 * FB >= tl.rows;             // no token of this wave: it only copies
     const int place = (q ^ (l16 & 7)) * 16;                // chunk q of a row; chunk q + 4 is at place ^ 64
     auto compute = [&](const char* st) {
         const float* sc = reinterpret_cast<const float*>(st + C::SCALES);
         const char* A = st + (ww * 16 * FA + l16) * 128;
-        const char* B = st + C::TW * 128 + (wt * 64 + l16) * 128;
-        uint4 b[FB][2];
+        const char* B = st + C::TW * 128 + (wt * 16 * FB + l16) * 128;
+        uint4 b[FB][2], av[2][2];
         float xs[FB];
+        f32x4_t part[2][FB];
+        auto fragment = [&](uint4 v[2], const char* p) {
+            v[0] = *reinterpret_cast<const uint4*>(p + place);
+            v[1] = *reinterpret_cast<const uint4*>(p + (place ^ 64));
+        };
 #pragma unroll
         for (int m = 0; m < FB; ++m) {
-            b[m][0] = *reinterpret_cast<const uint4*>(B + m * 2048 + place);
-            b[m][1] = *reinterpret_cast<const uint4*>(B + m * 2048 + (place ^ 64));
-            xs[m] = sc[wt * 64 + m * 16 + l16];
+            fragment(b[m], B + m * 2048);
+            xs[m] = sc[wt * 16 * FB + m * 16 + l16];
         }
+        fragment(av[0], A);
         const float w0 = sc[TT], w1 = sc[TT + 1];
-        if constexpr (OUT == OUT_F32) {
-            Wide bw[FB];
+        auto scale = [&](int j) { return GATED ? (j < HF ? w0 : w1) : (ww * 16 * FA + j * 16) < kBlock ? w0 : w1; };
+        auto add = [&](int j, int m) {
+            const float s = scale(j) * xs[m];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][m][i] += s * part[j & 1][m][i];
+        };
+        Wide bw[OUT == OUT_F32 ? FB : 1];
+        if constexpr (OUT == OUT_F32)
 #pragma unroll
             for (int m = 0; m < FB; ++m) bw[m] = widen_block(b[m]);
+        // the sums of fragment j - 1 are added between the products of fragment j
 #pragma unroll
-            for (int j = 0; j < FA; ++j) {
-                uint4 av[2];
-                av[0] = *reinterpret_cast<const uint4*>(A + j * 2048 + place);
-                av[1] = *reinterpret_cast<const uint4*>(A + j * 2048 + (place ^ 64));
-                const Wide aw = widen_block(av);
-                const float ws = (ww * 16 * FA + j * 16) < kBlock ? w0 : w1;
+        for (int j = 0; j < FA; ++j) {
+            if (j + 1 < FA) fragment(av[(j + 1) & 1], A + (j + 1) * 2048);
+            if constexpr (OUT == OUT_F32) {
+                const Wide aw = widen_block(av[j & 1]);
 #pragma unroll
                 for (int m = 0; m < FB; ++m) {
-                    const f32x4_t part = mfma_block(aw, bw[m]);
-                    const float s = ws * xs[m];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][m][i] += s * part[i];
+                    part[j & 1][m] = mfma_block(aw, bw[m]);
+                    if (j > 0) add(j - 1, m);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < FA; ++j) {
-                uint4 av[2];
-                av[0] = *reinterpret_cast<const uint4*>(A + j * 2048 + place);
-                av[1] = *reinterpret_cast<const uint4*>(A + j * 2048 + (place ^ 64));
-                const float ws = GATED ? (j < HF ? w0 : w1) : (ww * 16 * FA + j * 16) < kBlock ? w0 : w1;
+            } else {
 #pragma unroll
                 for (int m = 0; m < FB; ++m) {
-                    const f32x4_t part = mfma_codes(av, b[m]);
-                    const float s = ws * xs[m];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[j][m][i] += s * part[i];
+                    part[j & 1][m] = mfma_codes(av[j & 1], b[m]);
+                    if (j > 0) add(j - 1, m);
                 }
             }
         }
+#pragma unroll
+        for (int m = 0; m < FB; ++m) add(FA - 1, m);
     };
     // stage kb: wait for this wave's copies of it (those of the S - 2 stages behind it stay in
     // flight), then for every wave's; all have then left stage kb - 1, whose place is refilled
 #pragma unroll
     for (int i = 0; i < C::S - 1; ++i)
         if (i < kb_n) fill(i, i);
+    constexpr int BASE = NA + NB;                          // a wave copies BASE, or one or two more
     int stage = 0, ahead = C::S - 1;
     for (int kb = 0; kb < kb_n; ++kb) {
-        if (C::S > 2 && kb + 1 < kb_n) wait_and_meet<(C::S - 2) * C::COPIES>();
-        else wait_and_meet<0>();
+        if (C::S == 2 || kb + C::S - 2 >= kb_n) wait_and_meet<0>();
+        else if (copies == BASE) wait_and_meet<(C::S - 2) * BASE>();
+        else wait_and_meet<(C::S - 2) * (BASE + 1)>();
         if (kb + C::S - 1 < kb_n) fill(kb + C::S - 1, ahead);
         if (!idle) compute(lds + stage * C::STAGE);
         stage = stage + 1 == C::S ? 0 : stage + 1;
@@ -474,13 +353,13 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
                 }
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            if (q == 0) big[(wt * 64 + m * 16 + l16) * C::WW + ww] = top;
+            if (q == 0) big[(wt * 16 * FB + m * 16 + l16) * C::WW + ww] = top;
         }
         __syncthreads();
         uint8_t* out = static_cast<uint8_t*>(a.out);
 #pragma unroll
         for (int m = 0; m < FB; ++m) {
-            const int r = wt * 64 + m * 16 + l16;
+            const int r = wt * 16 * FB + m * 16 + l16;
             float top = 0.0f;
 #pragma unroll
             for (int i = 0; i < C::WW; ++i) top = fmaxf(top, big[r * C::WW + i]);
@@ -491,7 +370,7 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
             for (int j = 0; j < HF; ++j)
                 u[j] = f8_pack(acc[j][m][0] * inv, acc[j][m][1] * inv, acc[j][m][2] * inv, acc[j][m][3] * inv);
             const size_t row = tl.row0 + r;
-            uint32_t* o = reinterpret_cast<uint32_t*>(out + row * n_half + nb * C::COLS + ww * 16 * HF + q * V);
+            uint32_t* o = reinterpret_cast<uint32_t*>(out + row * n_half + nb * COLS + ww * 16 * HF + q * V);
             if constexpr (HF == 4) *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
             else if constexpr (HF == 2) *reinterpret_cast<uint2*>(o) = make_uint2(u[0], u[1]);
             else *o = u[0];
@@ -502,12 +381,12 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
         const bool wide = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && (size_t)a.N * es % 16 == 0;
 #pragma unroll
         for (int m = 0; m < FB; ++m) {
-            const int r = wt * 64 + m * 16 + l16;
+            const int r = wt * 16 * FB + m * 16 + l16;
             if (r >= tl.rows) continue;
             const size_t row = (size_t)(tl.row0 + r) * a.N;
 #pragma unroll
             for (int jc = 0; jc < FA / CF; ++jc) {
-                const int n = nb * C::COLS + ww * 16 * FA + jc * 16 * CF + q * 4 * CF;
+                const int n = nb * COLS + ww * 16 * FA + jc * 16 * CF + q * 4 * CF;
                 if (wide && n + 4 * CF <= a.N) {
                     if constexpr (OUT == OUT_F32) {
 #pragma unroll
@@ -521,10 +400,14 @@ __global__ __launch_bounds__(512, 2) void k_product_tile(ProductArgs a, int nblo
                             u[2 * j] = round_bf16(v[0]) | (uint32_t)round_bf16(v[1]) << 16;
                             u[2 * j + 1] = round_bf16(v[2]) | (uint32_t)round_bf16(v[3]) << 16;
                         }
+                        if constexpr (CF == 1) {
+                            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row + n) = make_uint2(u[0], u[1]);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < CF / 2; ++j)
-                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row + n + 8 * j) =
-                                make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+                            for (int j = 0; j < CF / 2; ++j)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row + n + 8 * j) =
+                                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+                        }
                     }
                 } else {
 #pragma unroll
@@ -546,26 +429,14 @@ int64_t most_tiles(const ProductArgs& a, int TM) {
     return (int64_t)a.M / TM + (a.G < a.M ? a.G : a.M);
 }
 
-template <int NT, int MT, int WN, int KS, int OUT>
-hipError_t stream(const ProductArgs& a, hipStream_t s) {
-    constexpr int COLS = OUT == OUT_SWIGLU ? 16 * WN : 16 * NT * WN;
+template <class C, int OUT>
+hipError_t product(const ProductArgs& a, hipStream_t s) {
+    constexpr int COLS = OUT == OUT_SWIGLU ? C::TW / 2 : C::TW;
     const int cols = OUT == OUT_SWIGLU ? a.N / 2 : a.N;
     const int nblocks = (cols + COLS - 1) / COLS, kb_n = (a.K + kBlock - 1) / kBlock;
-    const int64_t grid = nblocks * most_tiles(a, 16 * MT);
+    const int64_t grid = (nblocks * most_tiles(a, C::TT) + 7) / 8 * 8;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_product_stream<NT, MT, WN, KS, OUT>), dim3((unsigned)grid), dim3(64 * WN * KS), 0, s, a,
-                       nblocks, kb_n);
-    return hipGetLastError();
-}
-
-template <int TT, int OUT>
-hipError_t tiled(const ProductArgs& a, hipStream_t s) {
-    using C = TileShape<TT, OUT>;
-    const int cols = OUT == OUT_SWIGLU ? a.N / 2 : a.N;
-    const int nblocks = (cols + C::COLS - 1) / C::COLS, kb_n = (a.K + kBlock - 1) / kBlock;
-    const int64_t grid = (nblocks * most_tiles(a, TT) + 7) / 8 * 8;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_product_tile<TT, OUT>), dim3((unsigned)grid), dim3(512), 0, s, a, nblocks, kb_n);
+    hipLaunchKernelGGL((k_product<C, OUT>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, a, nblocks, kb_n);
     return hipGetLastError();
 }
 
@@ -573,11 +444,12 @@ template <int OUT>
 hipError_t by_rows(const ProductArgs& a, hipStream_t s) {
     const int64_t avg = a.M / a.G;
     if constexpr (OUT != OUT_F32)
-        if (avg >= 128) return tiled<256, OUT>(a, s);
-    if (avg >= 64) return tiled<128, OUT>(a, s);
-    if (avg >= 16) return tiled<64, OUT>(a, s);
-    if constexpr (OUT == OUT_SWIGLU) return stream<2, 1, 8, 2, OUT>(a, s);
-    else return stream<1, 1, 1, 4, OUT>(a, s);
+        if (avg >= 128) return product<Shape<256, 256, 8, 2>, OUT>(a, s);
+    if (avg >= 64) return product<Shape<256, 128, 8, 3>, OUT>(a, s);
+    if (avg >= 16) return product<Shape<256, 64, 8, 3>, OUT>(a, s);
+    if constexpr (OUT == OUT_SWIGLU) return product<Shape<256, 16, 8, 4>, OUT>(a, s);
+    else if ((int64_t)(a.N / 128) * (a.G < a.M ? a.G : a.M) >= 512) return product<Shape<128, 16, 4, 4>, OUT>(a, s);
+    else return product<Shape<64, 16, 4, 7>, OUT>(a, s);
 }
 
 }  // namespace
