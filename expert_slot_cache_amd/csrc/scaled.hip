@@ -11,12 +11,15 @@
 // on the order of k as long as both agree on it.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ops.hpp"
 #include "ops_dev.hpp"
 
 namespace moe {
 namespace {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -37,8 +40,8 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi) {
 struct Wide {
     bf16x8_t v[4];
 };
-__device__ __forceinline__ Wide widen_block(const uint4 a[2]) {
-    return {{widen8(a[0].x, a[0].y), widen8(a[0].z, a[0].w), widen8(a[1].x, a[1].y), widen8(a[1].z, a[1].w)}};
+__device__ __forceinline__ Wide widen_block(const i32x8_t& a) {
+    return {{widen8(a[0], a[1]), widen8(a[2], a[3]), widen8(a[4], a[5]), widen8(a[6], a[7])}};
 }
 __device__ __forceinline__ f32x4_t mfma_block(const Wide& a, const Wide& b) {
     f32x4_t c = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -47,20 +50,27 @@ __device__ __forceinline__ f32x4_t mfma_block(const Wide& a, const Wide& b) {
     return c;
 }
 
-// The row tiles of all groups, TM rows each, in group order.  Every wave counts them for
-// itself: a lane takes a run of groups, a prefix over the lanes orders the runs.  Offsets
-// outside [0, M] or falling ones (they are device data) count as empty groups, so that no
-// row outside the buffers is ever touched.
-struct Tile {
-    int group, row0, rows;
+// The work: the row tiles of all groups, TM rows each, times the column blocks of the matrix.
+// Every wave counts the tiles for itself: a lane takes a run of groups, a prefix over the lanes
+// orders the runs.  Offsets outside [0, M] or falling ones (they are device data) count as
+// empty groups, so that no row outside the buffers is ever touched.
+//
+// A group's work is listed up to four tiles at a time: those tiles of one column block, then
+// of the next.  Workgroups that run side by side on an XCD then read few different matrix and
+// token rows, and its L2 passes most requests on only once.
+struct Work {
+    int group, row0, rows, nb;
 };
 template <int TM>
-struct Tiles {
+struct Works {
+    static constexpr int SIDE = 4;
     const int32_t* offsets;
-    int M, g0, g1, lo0, hi0, own, incl, total;   // lo0, hi0: the rows of group g0
-    __device__ __forceinline__ Tiles(const int32_t* __restrict__ off, int G, int M_) : offsets(off), M(M_) {
+    int M, nblocks, total;
+    int g0, g1, lo0, hi0, own, incl;   // of this lane: its groups, the rows of the first, tiles, prefix of tiles
+    __device__ __forceinline__ Works(const int32_t* __restrict__ off, int G, int M_, int nblocks_)
+        : offsets(off), M(M_), nblocks(nblocks_) {
         if (!off) {
-            total = (M + TM - 1) / TM;
+            total = (M + TM - 1) / TM * nblocks;
             return;
         }
         const int lane = threadIdx.x & 63;
@@ -82,32 +92,37 @@ struct Tiles {
             const int o = __shfl_up(incl, d);
             if (lane >= d) incl += o;
         }
-        total = __builtin_amdgcn_readlane(incl, 63);
+        total = __builtin_amdgcn_readlane(incl, 63) * nblocks;
     }
     __device__ __forceinline__ int bound(int v, int lo) const { return min(max(v, lo), M); }
-    // Tile number `tile`, 0 <= tile < total.
-    __device__ __forceinline__ Tile at(int tile) const {
-        if (!offsets) return {0, tile * TM, min(TM, M - tile * TM)};
-        const int who = __builtin_ctzll(__ballot(incl > tile));
-        int group = 0, row0 = 0, rows = 0;
-        if ((int)(threadIdx.x & 63) == who) {
-            int left = tile - (incl - own);
-            int lo = lo0;
-            for (int g = g0; g < g1; ++g) {
-                const int hi = g == g0 ? hi0 : bound(offsets[g + 1], lo);
-                const int n = (hi - lo + TM - 1) / TM;
-                if (left < n) {
+    // Number i, 0 <= i < total.
+    __device__ __forceinline__ Work at(int i) const {
+        int group = 0, lo = 0, hi = M;
+        if (offsets) {
+            const int tile = i / nblocks;              // counting tiles alone: which group's
+            const int who = __builtin_ctzll(__ballot(incl > tile));
+            int first = incl - own;                    // the first tile of the lane's group g
+            if ((int)(threadIdx.x & 63) == who) {
+                lo = lo0;
+                for (int g = g0; g < g1; ++g) {
+                    hi = g == g0 ? hi0 : bound(offsets[g + 1], lo);
+                    const int n = (hi - lo + TM - 1) / TM;
                     group = g;
-                    row0 = lo + left * TM;
-                    rows = min(TM, hi - row0);
-                    break;
+                    if (tile < first + n) break;
+                    first += n;
+                    lo = hi;
                 }
-                left -= n;
-                lo = hi;
             }
+            group = __builtin_amdgcn_readlane(group, who);
+            lo = __builtin_amdgcn_readlane(lo, who);
+            hi = __builtin_amdgcn_readlane(hi, who);
+            i -= __builtin_amdgcn_readlane(first, who) * nblocks;
         }
-        return {__builtin_amdgcn_readlane(group, who), __builtin_amdgcn_readlane(row0, who),
-                __builtin_amdgcn_readlane(rows, who)};
+        const int n = (hi - lo + TM - 1) / TM;         // the group's tiles
+        const int side = i / (SIDE * nblocks) * SIDE, wide = min(SIDE, n - side);
+        i -= side * nblocks;
+        const int row0 = lo + (side + i % wide) * TM;
+        return {group, row0, min(TM, hi - row0), i / wide};
     }
 };
 
@@ -133,11 +148,9 @@ __device__ __forceinline__ float silu_mul(float gate, float up) { return gate / 
 // An fp32 output takes the bf16 instruction on the widened codes instead.
 typedef __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ f32x4_t mfma_codes(const uint4 a[2], const uint4 b[2]) {
-    const i32x8_t av = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w, (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
-    const i32x8_t bv = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w, (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
+__device__ __forceinline__ f32x4_t mfma_codes(const i32x8_t& a, const i32x8_t& b) {
     const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, zero, 0, 0, 0, 0, 0, 0);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
 // 16 (or 4) bytes per lane from memory to LDS: lane i's go to lds + 16 i (4 i).  The compiler
@@ -146,7 +159,7 @@ __device__ __forceinline__ f32x4_t mfma_codes(const uint4 a[2], const uint4 b[2]
 __device__ __forceinline__ void copy16(uint32_t lds, uint32_t voff, const uint8_t* base) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t lds, const uint8_t* p) {
+__device__ __forceinline__ void copy16(uint32_t lds, const float* p) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const float* p) {
@@ -159,21 +172,21 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-__device__ __align__(16) const uint8_t k_zeros[16] = {};   // what lies past the end of a row
-
 template <int TW_, int TT_, int WAVES_, int S_>
 struct Shape {
     static constexpr int TW = TW_, TT = TT_, WAVES = WAVES_, S = S_;
     static constexpr int WT = TT > 64 ? TT / 64 : 1;       // waves along tokens,
     static constexpr int WW = WAVES / WT;                  // along matrix rows
     static constexpr int FA = TW / WW / 16, FB = TT / WT / 16;   // fragments of a wave
+    static constexpr int AR = FA > 1 ? 2 : 1;              // matrix fragments in registers
     static constexpr int NA = TW / 8 / WAVES;              // a wave's copies of 8 matrix rows,
     static constexpr int NB = TT / 8 / WAVES;              // of 8 token rows (0: not every wave has one)
     static constexpr int XWAVES = TT / 8;                  // waves with one, where NB is 0
     static constexpr int SWAVES = (TT + 2 + 63) / 64;      // the last waves copy the scales, 64 each
-    static constexpr int SCALES = (TW + TT) * 128;         // their place in a stage: TT, then the matrix'
-    static constexpr int STAGE = SCALES + SWAVES * 256;
-    static constexpr int LDS = S * STAGE;
+    static constexpr int STAGE = (TW + TT) * 128;
+    static constexpr int SCALES = S * STAGE;               // their place: TT, then the matrix', per block
+    static constexpr int FOURS = S <= 5 ? 2 : 4;           // or four blocks at a time (see fill)
+    static constexpr int LDS = SCALES + SWAVES * 64 * 4 * (4 * FOURS > S ? 4 * FOURS : S);
     static_assert(FA >= 1 && FB >= 1 && NA >= 1 && (NB > 0 || XWAVES + SWAVES <= WAVES) && SWAVES <= WAVES, "");
 };
 
@@ -186,16 +199,14 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nb
     constexpr int COLS = GATED ? C::TW / 2 : C::TW;       // columns written
     static_assert(!GATED || (C::TW == 256 && HF >= 1), "a scale's 128 columns in one workgroup");
     __shared__ __align__(1024) char lds[C::LDS];
-    const Tiles<TT> tiles(a.offsets, a.G, a.M);
-    // workgroup b runs on XCD b % 8: each XCD takes one contiguous run of the (tile, column
-    // block) list, column block fastest, so that what shares rows or matrices shares an L2
-    const int nwork = tiles.total * nblocks;
-    const int per = (nwork + 7) >> 3;
+    const Works<TT> works(a.offsets, a.G, a.M, nblocks);
+    // workgroup b runs on XCD b % 8: each XCD takes one contiguous run of the work
+    const int per = (works.total + 7) >> 3;
     const int jx = (int)(blockIdx.x >> 3);
     const int wk = (int)(blockIdx.x & 7) * per + jx;
-    if (jx >= per || wk >= nwork) return;
-    const int nb = wk % nblocks;
-    const Tile tl = tiles.at(wk / nblocks);
+    if (jx >= per || wk >= works.total) return;
+    const Work tl = works.at(wk);
+    const int nb = tl.nb;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ww = wave % C::WW, wt = wave / C::WW;
@@ -234,102 +245,145 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nb
     const int second = GATED ? n_half / kBlock + nb : min(first + 1, nb_last);
     const float* sp = slot < TT ? a.xs + (size_t)(tl.row0 + min(max(slot, 0), tl.rows - 1)) * kb_n
                                 : sg + (size_t)(slot == TT + 1 ? second : first) * kb_n;
-    const int copies = NA + (NB > 0 ? NB : has_x ? 1 : 0) + (has_s ? 1 : 0);   // of this wave, a stage
-    const bool tail = K % kBlock != 0;
+    // A token's scale lies in a line of memory of its own, so four blocks' scales are copied at
+    // once where rows of scales start on 16 bytes (one block's cost as much as a third of its
+    // codes); FOURS such groups are kept, so that none is overwritten while S - 1 stages ahead
+    // of its last use.
+    const bool fours = kb_n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) % 16 == 0;
+    // In a last, shorter block the chunks past the end of a row are copied from its last 16
+    // bytes (`over` back from where they would be) and cleared in LDS once they have landed.
+    const int tail = K % kBlock;
+    const uint32_t over = tail && chunk >= tail ? chunk - (tail - 16) : 0;
 
     auto fill = [&](int kb, int stage) {
         const uint32_t at = lds0 + stage * C::STAGE;
         const size_t k0 = (size_t)kb * kBlock;
-        if (tail && kb == kb_n - 1) {
-            const bool in = (int)k0 + chunk < K;
+        const uint32_t back = kb == kb_n - 1 ? over : 0;
 #pragma unroll
-            for (int i = 0; i < NA; ++i) copy16(at + (wave + WAVES * i) * 1024, in ? abase[i] + aoff[i] + k0 : k_zeros);
-            if (has_x)
+        for (int i = 0; i < NA; ++i) copy16(at + (wave + WAVES * i) * 1024, aoff[i] - back, abase[i] + k0);
+        if (has_x)
 #pragma unroll
-                for (int i = 0; i < NB1; ++i)
-                    copy16(at + C::TW * 128 + (wave + WAVES * i) * 1024, in ? bbase + boff[i] + k0 : k_zeros);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NA; ++i) copy16(at + (wave + WAVES * i) * 1024, aoff[i], abase[i] + k0);
-            if (has_x)
-#pragma unroll
-                for (int i = 0; i < NB1; ++i) copy16(at + C::TW * 128 + (wave + WAVES * i) * 1024, boff[i], bbase + k0);
+            for (int i = 0; i < NB1; ++i) copy16(at + C::TW * 128 + (wave + WAVES * i) * 1024, boff[i] - back, bbase + k0);
+        if (has_s) {
+            const int sw = wave - (WAVES - C::SWAVES);
+            if (!fours) copy4(lds0 + C::SCALES + (stage * C::SWAVES + sw) * 256, sp + kb);
+            else if (kb % 4 == 0) copy16(lds0 + C::SCALES + (kb / 4 % C::FOURS * C::SWAVES + sw) * 1024, sp + kb);
         }
-        if (has_s) copy4(at + C::SCALES + (wave - (WAVES - C::SWAVES)) * 256, sp + kb);
     };
+
+    constexpr int BASE = NA + NB;                          // a wave's copies of rows, a stage; or one more
+    // Waits until all but the newest N stages of this wave's copies of rows have landed, and
+    // meets.  The scales' copies are not counted: a wave that made some waits for a little more.
+    auto landed = [&](auto stages) {
+        constexpr int N = decltype(stages)::value;
+        if (NB > 0 || !has_x) wait_and_meet<N * BASE>();
+        else wait_and_meet<N * (BASE + 1)>();
+    };
+    auto clear = [&](int stage) {                          // the last block's chunks past the end
+        __syncthreads();
+        for (int i = tid; i < (C::TW + TT) * 8; i += 64 * WAVES) {
+            const int r = i >> 3, c = i & 7;
+            if (c * 16 >= tail) *reinterpret_cast<i32x4_t*>(lds + stage * C::STAGE + r * 128 + ((c ^ (r & 7)) * 16)) = i32x4_t{0, 0, 0, 0};
+        }
+        __syncthreads();
+    };
+    // In the middle of stage kb, once a wave has read all that it needs of it: wait until this
+    // wave's copies of stage kb + 1 have landed (those of the S - 2 stages behind it stay in
+    // flight, but at the end of the row, where there are fewer), then for every wave's; the
+    // place of stage kb is refilled.
+    auto meet = [&](int kb, int stage, int next) {
+        if (kb + 1 >= kb_n) return;
+        if (kb + C::S - 1 < kb_n) landed(std::integral_constant<int, C::S - 2>{});
+        else wait_and_meet<0>();
+        if (kb + C::S < kb_n) fill(kb + C::S, stage);
+        if (tail && kb + 2 == kb_n) clear(next);
+    };
+#pragma unroll
+    for (int i = 0; i < C::S; ++i)
+        if (i < kb_n) fill(i, i);
+    if (kb_n >= C::S) landed(std::integral_constant<int, C::S - 1>{});
+    else wait_and_meet<0>();
+    if (tail && kb_n == 1) clear(0);
 
     f32x4_t acc[FA][FB];
 #pragma unroll
     for (int j = 0; j < FA; ++j)
 #pragma unroll
         for (int m = 0; m < FB; ++m) acc[j][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const bool idle = wt * 16 * FB >= tl.rows;             // no token of this wave: it only copies
-    const int place = (q ^ (l16 & 7)) * 16;                // chunk q of a row; chunk q + 4 is at place ^ 64
-    auto compute = [&](const char* st) {
-        const float* sc = reinterpret_cast<const float*>(st + C::SCALES);
-        const char* A = st + (ww * 16 * FA + l16) * 128;
-        const char* B = st + C::TW * 128 + (wt * 16 * FB + l16) * 128;
-        uint4 b[FB][2], av[2][2];
-        float xs[FB];
-        f32x4_t part[2][FB];
-        auto fragment = [&](uint4 v[2], const char* p) {
-            v[0] = *reinterpret_cast<const uint4*>(p + place);
-            v[1] = *reinterpret_cast<const uint4*>(p + (place ^ 64));
-        };
-#pragma unroll
-        for (int m = 0; m < FB; ++m) {
-            fragment(b[m], B + m * 2048);
-            xs[m] = sc[wt * 16 * FB + m * 16 + l16];
+    if (wt * 16 * FB >= tl.rows) {                         // no token for this wave: it only copies
+        for (int kb = 0, stage = 0; kb < kb_n; ++kb) {
+            const int next = stage + 1 == C::S ? 0 : stage + 1;
+            meet(kb, stage, next);
+            stage = next;
         }
-        fragment(av[0], A);
-        const float w0 = sc[TT], w1 = sc[TT + 1];
-        auto scale = [&](int j) { return GATED ? (j < HF ? w0 : w1) : (ww * 16 * FA + j * 16) < kBlock ? w0 : w1; };
-        auto add = [&](int j, int m) {
-            const float s = scale(j) * xs[m];
+        if constexpr (GATED) {                             // and meets the others where they share maxima
+            __syncthreads();
+            __syncthreads();
+        }
+        return;
+    }
+
+    constexpr int AR = C::AR, P = FA * FB < 3 ? FA * FB : 3;   // P: sums on their way to acc
+    const int place = (q ^ (l16 & 7)) * 16;                // chunk q of a row; chunk q + 4 is at place ^ 64
+    const int a0 = (ww * 16 * FA + l16) * 128 + place, b0 = C::TW * 128 + (wt * 16 * FB + l16) * 128 + place;
+    auto fragment = [&](i32x8_t& v, const char* at, int to) {
+        const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(at + to);
+        const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(at + (to ^ 64));
+        v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    i32x8_t b[FB], av[AR];
+    fragment(av[0], lds, a0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][m][i] += s * part[j & 1][m][i];
+    for (int m = 0; m < FB; ++m) fragment(b[m], lds, b0 + m * 2048);
+    int stage = 0;
+    for (int kb = 0; kb < kb_n; ++kb) {
+        // Product i (of fragments i / FB and i % FB), the adds of product i - 2, and the reads
+        // that the products to come need, those of the next stage among them, in this order:
+        // the compiler's own moves the reads next to their uses and the adds behind all products.
+        const int next = stage + 1 == C::S ? 0 : stage + 1;
+        const char* st = lds + stage * C::STAGE;
+        const char* nx = lds + next * C::STAGE;
+        const float* sc = reinterpret_cast<const float*>(lds + C::SCALES) +
+                          (fours ? kb / 4 % C::FOURS * C::SWAVES * 256 + kb % 4 : stage * C::SWAVES * 64);
+        const int each = fours ? 4 : 1;
+        float xs[FB];
+#pragma unroll
+        for (int m = 0; m < FB; ++m) xs[m] = sc[(wt * 16 * FB + m * 16 + l16) * each];
+        const float w0 = sc[TT * each], w1 = sc[(TT + 1) * each];
+        f32x4_t part[P];
+        Wide bw[OUT == OUT_F32 ? FB : 1], aw;
+        auto add = [&](int i) {
+            const int j = i / FB, m = i % FB;
+            const float ws = GATED ? (j < HF ? w0 : w1) : (ww * 16 * FA + j * 16) < kBlock ? w0 : w1;
+            const float s = ws * xs[m];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[j][m][k] += s * part[i % P][k];
+            asm volatile("" : "+v"(acc[j][m]));            // here, not sunk behind the meeting
         };
-        Wide bw[OUT == OUT_F32 ? FB : 1];
-        if constexpr (OUT == OUT_F32)
-#pragma unroll
-            for (int m = 0; m < FB; ++m) bw[m] = widen_block(b[m]);
-        // the sums of fragment j - 1 are added between the products of fragment j
 #pragma unroll
         for (int j = 0; j < FA; ++j) {
-            if (j + 1 < FA) fragment(av[(j + 1) & 1], A + (j + 1) * 2048);
-            if constexpr (OUT == OUT_F32) {
-                const Wide aw = widen_block(av[j & 1]);
+            if (AR > 1 && j + 1 < FA) fragment(av[(j + 1) % AR], st, a0 + (j + 1) * 2048);
+            if (j == FA - 1) meet(kb, stage, next);
+            if (AR > 1 && j + 1 == FA) fragment(av[(j + 1) % AR], nx, a0);
+            if constexpr (OUT == OUT_F32) aw = widen_block(av[j % AR]);
 #pragma unroll
-                for (int m = 0; m < FB; ++m) {
-                    part[j & 1][m] = mfma_block(aw, bw[m]);
-                    if (j > 0) add(j - 1, m);
+            for (int m = 0; m < FB; ++m) {
+                const int i = j * FB + m;
+                if constexpr (OUT == OUT_F32) {
+                    if (j == 0) bw[m] = widen_block(b[m]);
+                    part[i % P] = mfma_block(aw, bw[m]);
+                } else {
+                    part[i % P] = mfma_codes(av[j % AR], b[m]);
                 }
-            } else {
-#pragma unroll
-                for (int m = 0; m < FB; ++m) {
-                    part[j & 1][m] = mfma_codes(av[j & 1], b[m]);
-                    if (j > 0) add(j - 1, m);
-                }
+                if (j + 1 == FA) fragment(b[m], nx, b0 + m * 2048);
+                if (i >= P - 1) add(i - (P - 1));
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+        if (AR == 1) fragment(av[0], nx, a0);
 #pragma unroll
-        for (int m = 0; m < FB; ++m) add(FA - 1, m);
-    };
-    // stage kb: wait for this wave's copies of it (those of the S - 2 stages behind it stay in
-    // flight), then for every wave's; all have then left stage kb - 1, whose place is refilled
-#pragma unroll
-    for (int i = 0; i < C::S - 1; ++i)
-        if (i < kb_n) fill(i, i);
-    constexpr int BASE = NA + NB;                          // a wave copies BASE, or one or two more
-    int stage = 0, ahead = C::S - 1;
-    for (int kb = 0; kb < kb_n; ++kb) {
-        if (C::S == 2 || kb + C::S - 2 >= kb_n) wait_and_meet<0>();
-        else if (copies == BASE) wait_and_meet<(C::S - 2) * BASE>();
-        else wait_and_meet<(C::S - 2) * (BASE + 1)>();
-        if (kb + C::S - 1 < kb_n) fill(kb + C::S - 1, ahead);
-        if (!idle) compute(lds + stage * C::STAGE);
-        stage = stage + 1 == C::S ? 0 : stage + 1;
-        ahead = ahead + 1 == C::S ? 0 : ahead + 1;
+        for (int i = FA * FB - P + 1; i < FA * FB; ++i) add(i);
+        stage = next;
     }
 
     if constexpr (GATED) {
