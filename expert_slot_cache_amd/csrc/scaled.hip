@@ -187,7 +187,7 @@ struct Shape {
     static constexpr int SCALES = S * STAGE;               // their place: TT, then the matrix', per block
     static constexpr int FOURS = S <= 5 ? 2 : 4;           // or four blocks at a time (see fill)
     static constexpr int LDS = SCALES + SWAVES * 64 * 4 * (4 * FOURS > S ? 4 * FOURS : S);
-    static_assert(FA >= 1 && FB >= 1 && NA >= 1 && (NB > 0 || XWAVES + SWAVES <= WAVES) && SWAVES <= WAVES, "");
+    static_assert(FA >= 1 && FB >= 1 && NA >= 1 && (NB > 0 || XWAVES <= WAVES) && SWAVES <= WAVES, "");
 };
 
 template <class C, int OUT>
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nb
     // once where rows of scales start on 16 bytes (one block's cost as much as a third of its
     // codes); FOURS such groups are kept, so that none is overwritten while S - 1 stages ahead
     // of its last use.
-    const bool fours = kb_n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) % 16 == 0;
+    const bool fours = TT >= 64 && kb_n % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.ws)) % 16 == 0;
     // In a last, shorter block the chunks past the end of a row are copied from its last 16
     // bytes (`over` back from where they would be) and cleared in LDS once they have landed.
     const int tail = K % kBlock;
@@ -494,24 +494,46 @@ hipError_t product(const ProductArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The shape, by the rows that a group has on average and by the workgroups that a shape gives
+// (256 CUs).  The largest one wins whose tiles the groups fill and which still gives nearly
+// every CU a workgroup.  Measured (us; both sides of each border; 64 groups, hidden 2048 and
+// inter 1024 for both products of an expert, else N 4096 and K as said):
+//   256 x 256 / 256 x 128   32768 rows, K 4096: 660 / 738;  both products of 16384 rows: 231 / 223
+//   256 x 128 / 128 x 64    4096 rows, K 2048: 125 / 129;  one group, 1024 x 1024, K 4096: 36 / 22
+//   128 x 64 / 128 x 16     1024 rows, K 2048: 98 / 105;  32 rows of 25 groups, K 1024: 12.7 / 11.6
+//   128 x 64 / 64 x 32      one group, 333 x 1000, K 1040: 9.9 / 6.8
+//   64 x 32 / 32 x 16       one group, N 2048, K 2048: 128 rows 8.3 / 8.4, 64 rows 8.2 / 7.4
+//   SwiGLU 256 x 128 / 64   16384 rows: 223 / 262;  2048 rows: 102 / 102;  1024 rows: 91 / 92
+//   SwiGLU 256 x 64 / 32    one group: 2000 rows 30 / 41, 1000 rows 28 / 23
+//   SwiGLU 256 x 32 / 16    512 rows: 76 / 88;  64 rows: 51 / 50
 template <int OUT>
-hipError_t by_rows(const ProductArgs& a, hipStream_t s) {
+hipError_t by_size(const ProductArgs& a, hipStream_t s) {
     const int64_t avg = a.M / a.G;
-    if constexpr (OUT != OUT_F32)
-        if (avg >= 128) return product<Shape<256, 256, 8, 2>, OUT>(a, s);
-    if (avg >= 64) return product<Shape<256, 128, 8, 3>, OUT>(a, s);
-    if (avg >= 16) return product<Shape<256, 64, 8, 3>, OUT>(a, s);
-    if constexpr (OUT == OUT_SWIGLU) return product<Shape<256, 16, 8, 4>, OUT>(a, s);
-    else if ((int64_t)(a.N / 128) * (a.G < a.M ? a.G : a.M) >= 512) return product<Shape<128, 16, 4, 4>, OUT>(a, s);
-    else return product<Shape<64, 16, 4, 7>, OUT>(a, s);
+    auto fills = [&](int TW, int TT, int64_t least) {
+        return (int64_t)((a.N + TW - 1) / TW) * most_tiles(a, TT) >= least;
+    };
+    constexpr int64_t kMost = 192;
+    if constexpr (OUT != OUT_F32)   // the widened codes of 256 x 256 do not fit the registers
+        if (avg >= 384 && fills(256, 256, kMost)) return product<Shape<256, 256, 8, 2>, OUT>(a, s);
+    if (avg >= 32 && fills(256, 128, kMost)) return product<Shape<256, 128, 8, 3>, OUT>(a, s);
+    if constexpr (OUT == OUT_SWIGLU) {
+        if (avg >= 16 && fills(256, 64, kMost)) return product<Shape<256, 64, 8, 3>, OUT>(a, s);
+        if (avg >= 6 && fills(256, 32, kMost)) return product<Shape<256, 32, 8, 4>, OUT>(a, s);
+        return product<Shape<256, 16, 8, 4>, OUT>(a, s);
+    } else {
+        if (avg >= 16 && fills(128, 64, kMost)) return product<Shape<128, 64, 4, 3>, OUT>(a, s);
+        if (avg < 16 && fills(128, 16, kMost)) return product<Shape<128, 16, 4, 4>, OUT>(a, s);
+        if (fills(64, 32, 128)) return product<Shape<64, 32, 4, 5>, OUT>(a, s);
+        return product<Shape<32, 16, 2, 8>, OUT>(a, s);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_scaled_product(const ProductArgs& a, int out, hipStream_t s) {
-    if (out == OUT_SWIGLU) return by_rows<OUT_SWIGLU>(a, s);
-    if (out == OUT_BF16) return by_rows<OUT_BF16>(a, s);
-    return by_rows<OUT_F32>(a, s);
+    if (out == OUT_SWIGLU) return by_size<OUT_SWIGLU>(a, s);
+    if (out == OUT_BF16) return by_size<OUT_BF16>(a, s);
+    return by_size<OUT_F32>(a, s);
 }
 
 }  // namespace moe

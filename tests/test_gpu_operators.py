@@ -304,7 +304,9 @@ class Product:
 
 PRODUCTS = [(1, 1, 1, 16), (1, 1, 128, 128), (3, 1, 33, 144), (17, 4, 100, 272), (8, 64, 64, 512), (40, 3, 257, 1040),
             (200, 5, 384, 256), (333, 2, 130, 640), (700, 3, 512, 384), (1100, 2, 768, 256), (90, 1, 257, 1040),
-            (50, 3, 300, 1040), (600, 2, 520, 272), (150, 2, 1000, 16), (260, 1, 24, 128), (2049, 8, 264, 400)]
+            (50, 3, 300, 1040), (600, 2, 520, 272), (150, 2, 1000, 16), (260, 1, 24, 128), (2049, 8, 264, 400),
+            # enough workgroups for each larger tile: 128 x 16, 128 x 64, 256 x 128, 256 x 256
+            (200, 30, 1030, 528), (700, 30, 700, 528), (3500, 20, 1100, 272), (9000, 5, 1300, 144)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -321,6 +323,9 @@ def test_scaled_product(M, G, N, K, kind):
 
 @pytest.mark.parametrize("M,G,I,K", [(1, 1, 128, 128), (8, 64, 256, 512), (50, 3, 128, 1040), (300, 2, 384, 256),
                                      (180, 2, 256, 144), (70, 1, 128, 640), (1500, 4, 128, 272),
+                                     # the tiles of 32, 64, 128 and 256 rows
+                                     (300, 30, 768, 400), (700, 30, 640, 528), (3500, 20, 640, 272),
+                                     (9000, 5, 640, 144),
                                      (900, 3, 256, 384)])
 def test_scaled_product_swiglu(M, G, I, K):
     behind = 1 if G > 1 and M > 4 else 0
