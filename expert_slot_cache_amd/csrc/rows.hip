@@ -34,7 +34,7 @@ __host__ __device__ inline int64_t sort_chunk(int64_t P) {
 }
 
 // Dynamic LDS: base[E] int32, then cnt[kWaves][E] uint16.
-size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2 + 16; }
+size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2; }
 
 // Exclusive prefix sums of v[0 .. E) in place, by the whole workgroup; returns the sum.
 __device__ int block_scan(int32_t* v, int E) {
@@ -68,18 +68,19 @@ __device__ int block_scan(int32_t* v, int E) {
 }
 
 // One pass of ranking: the workgroup's pairs p0 .. p0 + kPass, wave by wave, 64 at a time.
-// id[r] (-1: not a pair of any expert) and rank[r] (the pair's place among this wave's of
+// id[r] (-1: not a pair of any expert), then rank[r] (the pair's place among this wave's of
 // its expert so far); cnt[wave][e] ends as the wave's count.  No barrier inside.
-__device__ __forceinline__ void rank_pass(const int32_t* __restrict__ ids, int64_t p0, int64_t end, int E, int bits,
-                                          uint16_t* cnt, int id[kRounds], int rank[kRounds]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t first = p0 + (int64_t)wave * (kRounds * 64) + lane;
+__device__ __forceinline__ void load_pass(const int32_t* __restrict__ ids, int64_t p0, int64_t end, int E, int id[kRounds]) {
+    const int64_t first = p0 + (int64_t)(threadIdx.x >> 6) * (kRounds * 64) + (threadIdx.x & 63);
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         const int64_t p = first + r * 64;
         const int v = p < end ? ids[p] : -1;
         id[r] = (unsigned)v < (unsigned)E ? v : -1;
     }
+}
+__device__ __forceinline__ void rank_pass(int E, int bits, uint16_t* cnt, const int id[kRounds], int rank[kRounds]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint16_t* mine = cnt + wave * E;
     for (int e = lane; e < E; e += 64) mine[e] = 0;
     __builtin_amdgcn_wave_barrier();   // LDS operations of one wave complete in order
@@ -245,7 +246,8 @@ __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* 
     uint16_t* cnt = reinterpret_cast<uint16_t*>(lds + E);
     const int P = a.T * a.K;
     int id[kRounds], rank[kRounds];
-    rank_pass(ids, 0, P, E, bits, cnt, id, rank);
+    load_pass(ids, 0, P, E, id);
+    rank_pass(E, bits, cnt, id, rank);
     __syncthreads();
     waves_turn(base, cnt, E, true);
     __syncthreads();
@@ -291,29 +293,39 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(const int32_t* __restri
     extern __shared__ int32_t lds[];
     int32_t* base = lds;
     uint16_t* cnt = reinterpret_cast<uint16_t*>(lds + E);
+    int32_t* before = reinterpret_cast<int32_t*>(cnt);   // [E], until cnt is used
     const int nb = gridDim.x, b = blockIdx.x;
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-        int sum = 0;
-        for (int i = 0; i < nb; ++i) sum += counts[(int64_t)i * E + e];
+    const int64_t p0 = b * chunk, end = p0 + chunk < P ? p0 + chunk : P;
+    int id[kRounds], rank[kRounds];
+    load_pass(ids, p0, end, E, id);
+    for (int e = threadIdx.x; e < E; e += kThreads) {   // of all workgroups, and of those before this one
+        int sum = 0, mine = 0;
+        for (int i = 0; i < nb; i += 16) {
+            int c[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) c[k] = counts[(int64_t)min(i + k, nb - 1) * E + e];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                sum += i + k < nb ? c[k] : 0;
+                mine += i + k < b ? c[k] : 0;
+            }
+        }
         base[e] = sum;
+        before[e] = mine;
     }
     __syncthreads();
     const int all = block_scan(base, E);
-    if (b == 0) {
-        for (int e = threadIdx.x; e < E; e += kThreads) offsets[e] = base[e];
-        if (threadIdx.x == 0) offsets[E] = all;
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+        const int first = base[e];
+        if (b == 0) offsets[e] = first;
+        base[e] = first + before[e];                    // this workgroup's first row of e
     }
+    if (b == 0 && threadIdx.x == 0) offsets[E] = all;
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) {   // this workgroup's first row of each expert
-        int before = 0;
-        for (int i = 0; i < b; ++i) before += counts[(int64_t)i * E + e];
-        base[e] += before;
-    }
-    const int64_t p0 = b * chunk, end = p0 + chunk < P ? p0 + chunk : P;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t q0 = p0; q0 < end; q0 += kPass) {
-        int id[kRounds], rank[kRounds];
-        rank_pass(ids, q0, end, E, bits, cnt, id, rank);
+        if (q0 > p0) load_pass(ids, q0, end, E, id);
+        rank_pass(E, bits, cnt, id, rank);
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
