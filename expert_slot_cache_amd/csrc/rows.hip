@@ -13,6 +13,8 @@
 // Everything else moves rows: a token is read once for all of its K copies.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ops.hpp"
 #include "ops_dev.hpp"
 
@@ -35,6 +37,23 @@ __host__ __device__ inline int64_t sort_chunk(int64_t P) {
 
 // Dynamic LDS: base[E] int32, then cnt[kWaves][E] uint16.
 size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2; }
+
+// Rows that are read once are loaded past the caches' retention, and a call whose pairs' rows
+// are more than the L2s hold (kStream bytes) also stores that way: nobody finds them there
+// again (sorting 4096 x 8 rows of 4096 to e4m3 35.7 us, 44.7 with plain stores; combining
+// 4001 x 8 rows of 2048, bf16, 40.2 us against 44.2).  A small call's rows stay for the next kernel.
+constexpr int64_t kStream = (int64_t)32 << 20;
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    const u32x4_t v = __builtin_nontemporal_load(static_cast<const u32x4_t*>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(void* p, uint4 q) {
+    const u32x4_t v = {q.x, q.y, q.z, q.w};
+    if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x4_t*>(p));
+    else *static_cast<u32x4_t*>(p) = v;
+}
 
 // Exclusive prefix sums of v[0 .. E) in place, by the whole workgroup; returns the sum.
 __device__ int block_scan(int32_t* v, int E) {
@@ -122,9 +141,9 @@ __device__ __forceinline__ void waves_turn(int32_t* base, uint16_t* cnt, int E, 
 // ---- a token's row to its K places -----------------------------------------------------
 // bx lanes side by side (a power of two) walk the row; rows: the token's K places.
 // Copies: 16-byte pieces when `wide`, else one element at a time.
-template <int AT>
+template <int AT, bool STREAM>
 __device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, bool wide, const int32_t* rows, int K,
-                                         int64_t P, void* out, int c, int bx) {
+                                         void* out, int c, int bx) {
     constexpr int es = AT == A_F32 ? 4 : 2;
     if (wide) {
         const char* src = static_cast<const char*>(x) + row * es;
@@ -133,7 +152,7 @@ __device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, bool
             const uint4 q = reinterpret_cast<const uint4*>(src)[c];
             for (int k = 0; k < K; ++k) {
                 const int r = rows[k];
-                if (r >= 0) *reinterpret_cast<uint4*>(static_cast<char*>(out) + ((int64_t)r * H * es + (int64_t)c * 16)) = q;
+                if (r >= 0) store16<STREAM>(static_cast<char*>(out) + ((int64_t)r * H * es + (int64_t)c * 16), q);
             }
         }
         return;
@@ -153,7 +172,7 @@ __device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, bool
 
 // e4m3: a lane takes 16 values, eight lanes side by side a block of 128 (bx is a multiple
 // of 8, H of 16; a last block may be shorter).
-template <int AT>
+template <int AT, bool STREAM>
 __device__ __forceinline__ void round_row(const void* x, int64_t row, int H, bool wide, const int32_t* rows, int K,
                                           uint8_t* out, float* scales, int c, int bx) {
     const int n = H / 16, nb = (H + kBlock - 1) / kBlock;
@@ -213,7 +232,7 @@ __device__ __forceinline__ void round_row(const void* x, int64_t row, int H, boo
         for (int k = 0; k < K; ++k) {
             const int64_t r = rows[k];
             if (r < 0) continue;
-            *reinterpret_cast<uint4*>(out + r * H + (int64_t)c * 16) = q;
+            store16<STREAM>(out + r * H + (int64_t)c * 16, q);
             if ((c & 7) == 0) scales[r * nb + (c >> 3)] = scale;
         }
     }
@@ -228,10 +247,10 @@ struct Spread {
     float* scales;
 };
 
-template <int AT, bool F8>
+template <int AT, bool F8, bool STREAM>
 __device__ __forceinline__ void spread_token(const Spread& a, int64_t t, const int32_t* rows, int c) {
-    if constexpr (F8) round_row<AT>(a.x, t * a.stride, a.H, a.wide, rows, a.K, static_cast<uint8_t*>(a.out), a.scales, c, a.bx);
-    else copy_row<AT>(a.x, t * a.stride, a.H, a.wide, rows, a.K, (int64_t)a.T * a.K, a.out, c, a.bx);
+    if constexpr (F8) round_row<AT, STREAM>(a.x, t * a.stride, a.H, a.wide, rows, a.K, static_cast<uint8_t*>(a.out), a.scales, c, a.bx);
+    else copy_row<AT, STREAM>(a.x, t * a.stride, a.H, a.wide, rows, a.K, a.out, c, a.bx);
 }
 
 // At most kOneLaunch pairs: every workgroup sorts them all (a few microseconds of ballots,
@@ -270,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* 
     if (!a.x) return;
     const int by = kThreads / a.bx;
     const int t = blockIdx.x * by + threadIdx.x / a.bx;
-    if (t < a.T) spread_token<AT, F8>(a, t, place + t * a.K, threadIdx.x & (a.bx - 1));
+    if (t < a.T) spread_token<AT, F8, false>(a, t, place + t * a.K, threadIdx.x & (a.bx - 1));
 }
 
 // More pairs: counts per workgroup, then places, then the rows (a launch each).
@@ -349,12 +368,12 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(const int32_t* __restri
     }
 }
 
-template <int AT, bool F8>
+template <int AT, bool F8, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_spread(Spread a, const int32_t* __restrict__ rows) {
     const int by = kThreads / a.bx;
     int64_t t = (int64_t)blockIdx.x * by + threadIdx.x / a.bx;
     if (a.bx >= 64) t = __builtin_amdgcn_readfirstlane((int)t);   // one token per wave: its places are scalars
-    if (t < a.T) spread_token<AT, F8>(a, t, rows + t * a.K, threadIdx.x & (a.bx - 1));
+    if (t < a.T) spread_token<AT, F8, STREAM>(a, t, rows + t * a.K, threadIdx.x & (a.bx - 1));
 }
 
 // ---- back: the weighted sum -------------------------------------------------------------
@@ -362,9 +381,10 @@ template <int AT, bool WIDE>
 struct Piece {
     static constexpr int N = WIDE ? (AT == A_F32 ? 4 : 8) : 1;
     float v[N];
-    __device__ __forceinline__ void load(const void* p, int64_t i) {   // i: element index
+    __device__ __forceinline__ void load(const void* p, int64_t i, bool once) {   // i: element index
         if constexpr (WIDE) {
-            const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (AT == A_F32 ? 4 : 2));
+            const char* at = static_cast<const char*>(p) + i * (AT == A_F32 ? 4 : 2);
+            const uint4 q = once ? load_once(at) : *reinterpret_cast<const uint4*>(at);
             const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int j = 0; j < N; ++j) v[j] = AT == A_F32 ? __uint_as_float(u[j & 3]) : widen_bf16((uint16_t)(u[j >> 1] >> (16 * (j & 1))));
@@ -372,6 +392,7 @@ struct Piece {
             v[0] = load_one<AT>(p, (size_t)i);
         }
     }
+    template <bool STREAM>
     __device__ __forceinline__ void store(void* p, int64_t i) const {
         if constexpr (WIDE) {
             uint32_t u[4];
@@ -380,16 +401,17 @@ struct Piece {
                 if constexpr (AT == A_F32) u[j] = __float_as_uint(v[j]);
                 else u[j] = round_bf16(v[2 * j]) | (uint32_t)round_bf16(v[2 * j + 1]) << 16;
             }
-            *reinterpret_cast<uint4*>(static_cast<char*>(p) + i * (AT == A_F32 ? 4 : 2)) = make_uint4(u[0], u[1], u[2], u[3]);
+            store16<STREAM>(static_cast<char*>(p) + i * (AT == A_F32 ? 4 : 2), make_uint4(u[0], u[1], u[2], u[3]));
         } else {
             store_one<AT>(p, (size_t)i, v[0]);
         }
     }
 };
 
-template <int AT, bool WIDE>
+template <int AT, bool WIDE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restrict__ ys, const int32_t* __restrict__ rows,
-        const float* __restrict__ w, const void* __restrict__ resid, int T, int K, int H, int bx, void* __restrict__ out) {
+        const float* __restrict__ w, const void* __restrict__ resid, int T, int K, int H, int bx,
+        void* __restrict__ out) {
     using V = Piece<AT, WIDE>;
     constexpr int KU = 8;   // rows in flight per lane
     const int by = kThreads / bx;
@@ -411,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restric
             const int r = k < K ? rows[(int64_t)t * K + k] : -1;
             on[j] = (unsigned)r < P;   // any other place: a pair that went to no expert
             wk[j] = on[j] && w ? w[(int64_t)t * K + k] : 1.0f;
-            if (on[j]) y[j].load(ys, (int64_t)r * H + c);
+            if (on[j]) y[j].load(ys, (int64_t)r * H + c, true);
         }
 #pragma unroll
         for (int j = 0; j < KU; ++j)
@@ -421,17 +443,17 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restric
     }
     if (resid) {
         V r;
-        r.load(resid, (int64_t)t * H + c);
+        r.load(resid, (int64_t)t * H + c, true);
 #pragma unroll
         for (int i = 0; i < V::N; ++i) acc.v[i] += r.v[i];
     }
-    acc.store(out, (int64_t)t * H + c);
+    acc.template store<STREAM>(out, (int64_t)t * H + c);
 }
 
 // A wave takes a token and up to eight of its pairs (grid.y walks the groups of pairs):
 // d_out[t] is read once for them, each pair's dot product stays in a register per lane and
 // is summed over the wave at the end, in a fixed order.
-template <int AT, bool WIDE>
+template <int AT, bool WIDE, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_combine_rows_backward(const void* __restrict__ dout,
         const void* __restrict__ ys, const int32_t* __restrict__ rows, const float* __restrict__ w, int T, int K, int per,
         int H, void* __restrict__ dys, float* __restrict__ dw) {
@@ -454,10 +476,10 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows_backward(const void* 
     }
     for (int c = lane * V::N; c < H; c += 64 * V::N) {
         V d, y[KU];
-        d.load(dout, (int64_t)t * H + c);
+        d.load(dout, (int64_t)t * H + c, false);
 #pragma unroll
         for (int j = 0; j < KU; ++j)
-            if (at[j] >= 0) y[j].load(ys, at[j] + c);
+            if (at[j] >= 0) y[j].load(ys, at[j] + c, true);
 #pragma unroll
         for (int j = 0; j < KU; ++j) {
             if (at[j] < 0) continue;
@@ -467,7 +489,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows_backward(const void* 
                 dot[j] += y[j].v[i] * d.v[i];
                 o.v[i] = wk[j] * d.v[i];
             }
-            o.store(dys, at[j] + c);
+            o.template store<STREAM>(dys, at[j] + c);
         }
     }
 #pragma unroll
@@ -512,27 +534,46 @@ hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, i
     hipLaunchKernelGGL(k_sort_count, dim3(nb), dim3(kThreads), (size_t)E * 4, s, ids, P, chunk, E, counts);
     hipLaunchKernelGGL(k_sort_place, dim3(nb), dim3(kThreads), sort_lds(E), s, ids, P, chunk, E, bits, counts, offsets,
                        rows);
-    if (a.x) hipLaunchKernelGGL((k_spread<AT, F8>), dim3(tokens_grid), dim3(kThreads), 0, s, a, rows);
+    if (!a.x) return hipGetLastError();
+    if (P * a.H * (F8 ? 1 : es) > kStream)
+        hipLaunchKernelGGL((k_spread<AT, F8, true>), dim3(tokens_grid), dim3(kThreads), 0, s, a, rows);
+    else
+        hipLaunchKernelGGL((k_spread<AT, F8, false>), dim3(tokens_grid), dim3(kThreads), 0, s, a, rows);
     return hipGetLastError();
 }
 
-template <int AT, bool WIDE>
+template <int AT, bool WIDE, bool STREAM>
 hipError_t combine(const void* ys, const int32_t* rows, const float* w, const void* resid, int T, int K, int H,
                    void* out, hipStream_t s) {
     const int n = H / Piece<AT, WIDE>::N;
     const int bx = lanes_for(n, 8), by = kThreads / bx;
-    hipLaunchKernelGGL((k_combine_rows<AT, WIDE>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0, s, ys,
-                       rows, w, resid, T, K, H, bx, out);
+    hipLaunchKernelGGL((k_combine_rows<AT, WIDE, STREAM>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0,
+                       s, ys, rows, w, resid, T, K, H, bx, out);
     return hipGetLastError();
 }
 
-template <int AT, bool WIDE>
+template <int AT, bool WIDE, bool STREAM>
 hipError_t combine_backward(const void* dout, const void* ys, const int32_t* rows, const float* w, int T, int K, int H,
                             void* dys, float* dw, hipStream_t s) {
     const int groups = (K + 7) / 8, per = (K + groups - 1) / groups;
-    hipLaunchKernelGGL((k_combine_rows_backward<AT, WIDE>), dim3((T + kWaves - 1) / kWaves, groups), dim3(kThreads), 0,
-                       s, dout, ys, rows, w, T, K, per, H, dys, dw);
+    hipLaunchKernelGGL((k_combine_rows_backward<AT, WIDE, STREAM>), dim3((T + kWaves - 1) / kWaves, groups),
+                       dim3(kThreads), 0, s, dout, ys, rows, w, T, K, per, H, dys, dw);
     return hipGetLastError();
+}
+
+// Calls f<AT, WIDE, STREAM>: 16-byte pieces where rows and bases allow them, and large calls'
+// stores past the caches (single elements are too slow for that to matter).
+template <class F>
+hipError_t by_form(int atype, bool wide, bool stream, F f) {
+    using std::integral_constant;
+    using Yes = integral_constant<bool, true>;
+    using No = integral_constant<bool, false>;
+    if (atype == A_F32) {
+        const integral_constant<int, A_F32> at;
+        return !wide ? f(at, No{}, No{}) : stream ? f(at, Yes{}, Yes{}) : f(at, Yes{}, No{});
+    }
+    const integral_constant<int, A_BF16> at;
+    return !wide ? f(at, No{}, No{}) : stream ? f(at, Yes{}, Yes{}) : f(at, Yes{}, No{});
 }
 
 }  // namespace
@@ -558,20 +599,19 @@ hipError_t launch_combine(int atype, const void* ys, const int32_t* rows, const 
                           int K, int H, void* out, hipStream_t s) {
     const int es = atype == A_F32 ? 4 : 2;
     const bool wide = (int64_t)H * es % 16 == 0 && on16(ys) && on16(out) && (!resid || on16(resid));
-    if (atype == A_F32)
-        return wide ? combine<A_F32, true>(ys, rows, w, resid, T, K, H, out, s) : combine<A_F32, false>(ys, rows, w, resid, T, K, H, out, s);
-    return wide ? combine<A_BF16, true>(ys, rows, w, resid, T, K, H, out, s) : combine<A_BF16, false>(ys, rows, w, resid, T, K, H, out, s);
+    return by_form(atype, wide, (int64_t)T * K * H * es > kStream, [&](auto at, auto wd, auto st) {
+        return combine<decltype(at)::value, decltype(wd)::value, decltype(st)::value>(ys, rows, w, resid, T, K, H, out, s);
+    });
 }
 
 hipError_t launch_combine_backward(int atype, const void* dout, const void* ys, const int32_t* rows, const float* w,
                                    int T, int K, int H, void* dys, float* dw, hipStream_t s) {
     const int es = atype == A_F32 ? 4 : 2;
     const bool wide = (int64_t)H * es % 16 == 0 && on16(dout) && on16(ys) && on16(dys);
-    if (atype == A_F32)
-        return wide ? combine_backward<A_F32, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
-                    : combine_backward<A_F32, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
-    return wide ? combine_backward<A_BF16, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
-                : combine_backward<A_BF16, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
+    return by_form(atype, wide, (int64_t)T * K * H * es > kStream, [&](auto at, auto wd, auto st) {
+        return combine_backward<decltype(at)::value, decltype(wd)::value, decltype(st)::value>(dout, ys, rows, w, T, K, H,
+                                                                                             dys, dw, s);
+    });
 }
 
 }  // namespace moe

@@ -126,7 +126,12 @@ struct Works {
     }
 };
 
-__device__ __forceinline__ float silu_mul(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+// silu(gate) * up with the hardware's exponential and reciprocal (1 ulp each): within about
+// (4 + |gate|) 2^-24 of the value, far below the half step 2^-4 of the e4m3 code it becomes; the
+// exact quotient and exponential took as long as three stages of a tile.
+__device__ __forceinline__ float silu_mul(float gate, float up) {
+    return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;
+}
 
 // ---- the kernel ------------------------------------------------------------------------------
 //
