@@ -402,6 +402,8 @@ def _bad(what: str):
 def _check_tensor(name: str, t, dtype, shape, dev: int, rows: bool = False):
     """t lies on device `dev`, is of this dtype and shape, and contiguous (`rows`: only
     within its rows)."""
+    if t is None:
+        _bad(f"{name} is missing")
     if t.get_device() != dev:
         _bad(f"{name} is not on the current device, cuda:{dev}")
     if t.dtype is not dtype:
@@ -491,7 +493,10 @@ def sort_tokens(x, topk_ids, sorted_x, offsets, rows, *, scales=None, workspace=
     E = offsets.numel() - 1
     _check_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     H = at = f8 = stride = 0
-    if x is not None:
+    if x is None:
+        if sorted_x is not None or scales is not None:
+            _bad("sorted rows need x")
+    else:
         H = _matrix("x", x)[1]
         at, stride = _atype(torch, "x", x), _stride(x)
         _check_tensor("x", x, x.dtype, (T, H), dev, rows=True)

@@ -36,13 +36,14 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 __device__ __forceinline__ float logit_of(uint32_t k) {
     return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
-// exp(l - m) for l <= m as 2^(l log2 e - m log2 e).  What the rounding of m log2 e does is
-// common to all terms of a row and to their sum; the rest is within |l - m| 2^-24 of the value.
-// With m infinite: equal logits count 1 each, the limit at +inf, and a row of -inf alone has no
-// softmax, every term is 0.
+// exp(l - m) for l <= m: the difference first, so that rows of any size keep in range (a whole
+// row of the type's lowest value is a uniform one), then 2^(d log2 e), within |d| 2^-23 of the
+// value.  With m infinite: equal logits count 1 each, the limit at +inf, and a row of -inf alone
+// has no softmax, every term is 0.
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float finite_term(float l, float m) { return __builtin_amdgcn_exp2f((l - m) * kLog2e); }
 __device__ __forceinline__ float term(float l, float m) {
-    constexpr float kLog2e = 1.44269504f;
-    if (fabsf(m) < __builtin_inff()) return __builtin_amdgcn_exp2f(fmaf(l, kLog2e, -(m * kLog2e)));
+    if (fabsf(m) < __builtin_inff()) return finite_term(l, m);
     return m > 0.0f && l == m ? 1.0f : 0.0f;
 }
 
@@ -169,9 +170,8 @@ __device__ __forceinline__ float softmax_sum(const float l[V], bool all, float* 
     if (all) {
         float s = 0.0f;
         if (__all(fabsf(m) < __builtin_inff())) {      // the same terms, without their special cases
-            const float m2 = m * 1.44269504f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) s += __builtin_amdgcn_exp2f(fmaf(l[j], 1.44269504f, -m2));
+            for (int j = 0; j < V; ++j) s += finite_term(l[j], m);
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j) s += term(l[j], m);

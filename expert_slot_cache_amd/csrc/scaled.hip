@@ -66,7 +66,7 @@ struct Works {
     static constexpr int SIDE = 4;
     const int32_t* offsets;
     int M, nblocks, total;
-    int g0, g1, lo0, hi0, own, incl;   // of this lane: its groups, the rows of the first, tiles, prefix of tiles
+    int g0, g1, lo0, own, incl;        // of this lane: its groups, the first one's row, tiles, prefix of tiles
     __device__ __forceinline__ Works(const int32_t* __restrict__ off, int G, int M_, int nblocks_)
         : offsets(off), M(M_), nblocks(nblocks_) {
         if (!off) {
@@ -78,14 +78,12 @@ struct Works {
         g0 = min(lane * per, G);
         g1 = min(g0 + per, G);
         lo0 = bound(off[g0], 0);
-        hi0 = g0 < g1 ? bound(off[g0 + 1], lo0) : lo0;
-        own = (hi0 - lo0 + TM - 1) / TM;
-        int lo = hi0;
-        for (int g = g0 + 1; g < g1; ++g) {
-            const int hi = bound(off[g + 1], lo);
-            own += (hi - lo + TM - 1) / TM;
-            lo = hi;
-        }
+        own = 0;
+        int lo = lo0;
+        walk(lo, [&](int, int, int n) {
+            own += n;
+            return false;
+        });
         incl = own;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -95,6 +93,23 @@ struct Works {
         total = __builtin_amdgcn_readlane(incl, 63) * nblocks;
     }
     __device__ __forceinline__ int bound(int v, int lo) const { return min(max(v, lo), M); }
+    // f(group, the row behind its last, its tiles) over this lane's groups, until f says so; `lo` follows.
+    // Eight offsets are requested at a time.
+    template <class F>
+    __device__ __forceinline__ void walk(int& lo, F f) const {
+        for (int g = g0; g < g1; g += 8) {
+            int end[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) end[k] = offsets[min(g + 1 + k, g1)];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (g + k >= g1) return;
+                const int hi = bound(end[k], lo);
+                if (f(g + k, hi, (hi - lo + TM - 1) / TM)) return;
+                lo = hi;
+            }
+        }
+    }
     // Number i, 0 <= i < total.
     __device__ __forceinline__ Work at(int i) const {
         int group = 0, lo = 0, hi = M;
@@ -104,14 +119,13 @@ struct Works {
             int first = incl - own;                    // the first tile of the lane's group g
             if ((int)(threadIdx.x & 63) == who) {
                 lo = lo0;
-                for (int g = g0; g < g1; ++g) {
-                    hi = g == g0 ? hi0 : bound(offsets[g + 1], lo);
-                    const int n = (hi - lo + TM - 1) / TM;
+                walk(lo, [&](int g, int end, int n) {
                     group = g;
-                    if (tile < first + n) break;
+                    hi = end;
+                    if (tile < first + n) return true;
                     first += n;
-                    lo = hi;
-                }
+                    return false;
+                });
             }
             group = __builtin_amdgcn_readlane(group, who);
             lo = __builtin_amdgcn_readlane(lo, who);

@@ -45,6 +45,7 @@ def logits_for(T, E, seed, special=True):
     rng = np.random.default_rng(seed)
     z = (2 * rng.normal(size=(T, E))).astype(np.float32)
     if special and T >= 8:
+        z[0] = -3.38e38                               # a whole row of (nearly) the lowest value
         z[1] = 0.5                                    # all equal
         z[2] = -INF                                   # masked altogether
         z[3, ::2] = -INF                              # half masked
@@ -306,7 +307,7 @@ PRODUCTS = [(1, 1, 1, 16), (1, 1, 128, 128), (3, 1, 33, 144), (17, 4, 100, 272),
             (200, 5, 384, 256), (333, 2, 130, 640), (700, 3, 512, 384), (1100, 2, 768, 256), (90, 1, 257, 1040),
             (50, 3, 300, 1040), (600, 2, 520, 272), (150, 2, 1000, 16), (260, 1, 24, 128), (2049, 8, 264, 400),
             # enough workgroups for each larger tile: 128 x 16, 128 x 64, 256 x 128, 256 x 256
-            (200, 30, 1030, 528), (700, 30, 700, 528), (3500, 20, 1100, 272), (9000, 5, 1300, 144)]
+            (200, 30, 1030, 528), (700, 600, 40, 144), (700, 30, 700, 528), (3500, 20, 1100, 272), (9000, 5, 1300, 144)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -541,6 +542,8 @@ def test_binding_refuses_what_does_not_fit():
                                     workspace=torch.zeros(8, dtype=torch.uint8, device=DEV)),
         lambda: binding.sort_tokens(None, i32(4000, 2), None, i32(9), i32(4000, 2),
                                     stream=torch.cuda.Stream().cuda_stream),
+        lambda: binding.sort_tokens(f32(4, 16), i32(4, 2), None, i32(9), i32(4, 2)),
+        lambda: binding.sort_tokens(None, i32(4, 2), f32(8, 16), i32(9), i32(4, 2)),
         lambda: binding.combine_rows(f32(8, 16), i32(4, 2), f32(4, 16).bfloat16()),
         lambda: binding.combine_rows(f32(8, 16), i32(4, 2), f32(4, 16), resid=f32(4, 8)),
         lambda: binding.combine_rows_backward(f32(4, 16), f32(8, 16), i32(4, 2), f32(4, 2), f32(8, 15), f32(4, 2)),
