@@ -402,6 +402,9 @@ def _bad(what: str):
 def _check_tensor(name: str, t, dtype, shape, dev: int, rows: bool = False):
     """t lies on device `dev`, is of this dtype and shape, and contiguous (`rows`: only
     within its rows)."""
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.shape == shape and \
+            (t.is_contiguous() or rows and t.stride(1) == 1):
+        return
     if t is None:
         _bad(f"{name} is missing")
     if t.get_device() != dev:
@@ -410,11 +413,10 @@ def _check_tensor(name: str, t, dtype, shape, dev: int, rows: bool = False):
         _bad(f"{name} is {t.dtype}, not {dtype}")
     if t.shape != shape:
         _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    if rows:
-        if shape[1] > 1 and t.stride(1) != 1:
-            _bad(f"the values of a row of {name} are not contiguous")
-    elif not t.is_contiguous():
+    if not rows:
         _bad(f"{name} is not contiguous")
+    if shape[1] > 1:
+        _bad(f"the values of a row of {name} are not contiguous")
 
 
 def _stride(t) -> int:

@@ -279,9 +279,9 @@ def eights(v):
 
 class Product:
     """Inputs of a product, its value in 64 bits and bounds on a kernel's error.  `bound`, for
-    fp32 outputs: a block's 128 products are summed by the matrix core (at most two half steps
-    an addition: it may truncate), the blocks and scales in fp32.  `coarse`, for the bf16 and
-    e4m3 outputs: the fp8 matrix instruction drops what lies 13 bits below the largest of each
+    fp32 and SwiGLU outputs: a block's 128 products are summed by the matrix core (at most two half steps
+    an addition: it may truncate), the blocks and scales in fp32.  `coarse`, for bf16
+    outputs: the fp8 matrix instruction drops what lies 13 bits below the largest of each
     eight products, less than 8 * 2^-13 of that largest an eight, and the largest product of an
     eight is at most the product of the largest factors."""
 
@@ -337,7 +337,7 @@ def test_scaled_product_swiglu(M, G, I, K):
     got, sc = host(out), host(scales)
     live = ~np.isnan(p.ref[:, 0])
     assert (got[~live] == 7.0).all() and (sc[~live] == 7.0).all()
-    got, sc, h, e = got[live], sc[live], p.ref[live], p.coarse[live]
+    got, sc, h, e = got[live], sc[live], p.ref[live], p.bound[live]
     a = orows.swiglu(h)
     # |d a| <= 1.1 |up| d gate + |silu| d up, then a few roundings of the value
     err = 1.1 * np.abs(h[:, I:]) * e[:, :I] + np.abs(h[:, :I]) * e[:, I:] + 1.1 * e[:, :I] * e[:, I:] + 16 * U * np.abs(a)
