@@ -52,6 +52,71 @@ __device__ __forceinline__ void store_one(void* p, size_t i, float v) {
     else static_cast<uint16_t*>(p)[i] = round_bf16(v);
 }
 
+// Sixteen bytes at a time wherever an element may start: rows of any length and stride move in
+// whole 16-byte pieces but for the last, shorter one (global accesses need no more alignment
+// than their elements').  `once`: past the caches' retention.
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+template <int AT>
+struct Bits;
+template <>
+struct Bits<A_F32> {
+    typedef uint32_t one;
+    typedef uint32_t four __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <>
+struct Bits<A_BF16> {
+    typedef uint16_t one;
+    typedef uint32_t four __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <int AT>
+__device__ __forceinline__ u32x4_t load16(const void* p, bool once) {
+    const auto* q = static_cast<const typename Bits<AT>::four*>(p);
+    return once ? __builtin_nontemporal_load(q) : *q;
+}
+template <int AT, bool ONCE>
+__device__ __forceinline__ void store16(void* p, u32x4_t v) {
+    auto* q = static_cast<typename Bits<AT>::four*>(p);
+    if constexpr (ONCE) __builtin_nontemporal_store(v, q);
+    else *q = v;
+}
+
+// Sixteen bytes of a row as fp32 values.  FULL: all of them lie in the row; otherwise `left` do.
+template <int AT>
+struct Piece {
+    static constexpr int ES = AT == A_F32 ? 4 : 2, N = 16 / ES;
+    float v[N];
+    template <bool FULL>
+    __device__ __forceinline__ void load(const void* p, int64_t i, int left, bool once) {   // i: element index
+        if constexpr (FULL) {
+            const u32x4_t q = load16<AT>(static_cast<const char*>(p) + i * ES, once);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if constexpr (AT == A_F32) v[j] = __uint_as_float(q[j]);
+                else v[j] = widen_bf16((uint16_t)(q[j >> 1] >> (16 * (j & 1))));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = j < left ? load_one<AT>(p, (size_t)i + j) : 0.0f;
+        }
+    }
+    template <bool FULL, bool ONCE>
+    __device__ __forceinline__ void store(void* p, int64_t i, int left) const {
+        if constexpr (FULL) {
+            u32x4_t q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (AT == A_F32) q[j] = __float_as_uint(v[j]);
+                else q[j] = round_bf16(v[2 * j]) | (uint32_t)round_bf16(v[2 * j + 1]) << 16;
+            }
+            store16<AT, ONCE>(static_cast<char*>(p) + i * ES, q);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < left) store_one<AT>(p, (size_t)i + j, v[j]);
+        }
+    }
+};
+
 // The e4m3 scale of a block whose largest finite magnitude is `big`: the smallest power
 // of two that brings it to 448 = 1.75 * 2^8 or less, 1 for a block of zeros.  A power of
 // two divides exactly, so the only rounding is the one to e4m3 (half a step at most:

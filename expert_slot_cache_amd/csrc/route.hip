@@ -131,25 +131,31 @@ struct Eights {
 };
 
 // A token's logits: V consecutive ones per lane; NaN counts as -inf (fmaxf drops it), both zeros
-// are equal (-0 + 0 = 0), and past the end there are -inf.  `wide` (host: base and stride allow
-// it and E is a multiple of V): 16-byte loads.
+// are equal (-0 + 0 = 0), and past the end there are -inf.
 template <int AT, int V>
-__device__ __forceinline__ void load_logits(const void* logits, size_t row, int E, int lane, bool wide, float l[V]) {
-    constexpr int PER = AT == A_F32 ? 4 : 8;
+__device__ __forceinline__ void load_logits(const void* logits, size_t row, int E, int lane, float l[V]) {
+    constexpr int N = Piece<AT>::N;
     const int e0 = lane * V;
 #pragma unroll
     for (int j = 0; j < V; ++j) l[j] = -__builtin_inff();
-    if (V >= PER && wide) {
-        if (e0 < E) {
-            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(logits) + (row + e0) * (AT == A_F32 ? 4 : 2));
+    auto piece = [&](int c) {                              // a lane comes back to its lines: not `once`
+        Piece<AT> p;
+        p.template load<true>(logits, (int64_t)(row + e0 + c), N, false);
 #pragma unroll
-            for (int c = 0; c < V / PER; ++c) {
-                const uint4 q = p[c];
-                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        for (int j = 0; j < N; ++j) l[c + j] = p.v[j];
+    };
+    if (V >= N && E % V == 0) {                            // no lane has a part of its share: no choice per piece
+        if (e0 < E)
 #pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    l[c * PER + i] = AT == A_F32 ? __uint_as_float(u[i & 3]) : widen_bf16((uint16_t)(u[i >> 1] >> (16 * (i & 1))));
-            }
+            for (int c = 0; c + N <= V; c += N) piece(c);
+    } else if (V >= N) {
+#pragma unroll
+        for (int c = 0; c + N <= V; c += N) {
+            if (e0 + c + N <= E) piece(c);
+            else if (e0 + c < E)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (e0 + c + j < E) l[c + j] = load_one<AT>(logits, row + e0 + c + j);
         }
     } else {
 #pragma unroll
@@ -183,7 +189,7 @@ __device__ __forceinline__ float softmax_sum(const float l[V], bool all, float* 
 
 template <int AT, int L, int V, bool RENORM>
 __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route(const void* __restrict__ logits, int64_t stride, int T,
-        int E, int K, bool wide, int32_t* __restrict__ ids, float* __restrict__ w) {
+        int E, int K, int32_t* __restrict__ ids, float* __restrict__ w) {
     constexpr int PER = 64 / L;                        // tokens of a wave
     __shared__ uint2 found[kTokensPerBlock][PER][kMaxTopK];   // (id, key) in order
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route(const void* __re
     const int t = (blockIdx.x * kTokensPerBlock + wave) * PER + sub;
     const bool here = t < T;                           // the wave's other lanes go through the motions
     float logit[V], sum = 0.0f;
-    load_logits<AT, V>(logits, (size_t)(here ? t : 0) * (size_t)stride, here ? E : 0, l, wide, logit);
+    load_logits<AT, V>(logits, (size_t)(here ? t : 0) * (size_t)stride, here ? E : 0, l, logit);
     const float m = softmax_sum<L, V>(logit, !RENORM, &sum);
     Eights<V> keys;
 #pragma unroll
@@ -231,7 +237,7 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route(const void* __re
 template <int AT, int V, bool RENORM>
 __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_backward(const void* __restrict__ logits, int64_t stride,
         const int32_t* __restrict__ ids, const float* __restrict__ w, const float* __restrict__ dw, int T, int E, int K,
-        bool wide, bool wide_out, void* __restrict__ dl, int64_t dstride) {
+        void* __restrict__ dl, int64_t dstride) {
     extern __shared__ float lds[];
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * kTokensPerBlock + (threadIdx.x >> 6);
@@ -266,7 +272,7 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_backward(const v
     for (int j = 0; j < V; ++j) d[j] = g[lane * V + j];
     if constexpr (!RENORM) {
         float l[V], sum = 0.0f;
-        load_logits<AT, V>(logits, (size_t)t * (size_t)stride, E, lane, wide, l);
+        load_logits<AT, V>(logits, (size_t)t * (size_t)stride, E, lane, l);
         const float m = softmax_sum<64, V>(l, true, &sum);
         const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
@@ -277,33 +283,22 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_backward(const v
     }
     const size_t row = (size_t)t * (size_t)dstride;
     const int e0 = lane * V;
-    constexpr int PER = AT == A_F32 ? 4 : 8;
-    if constexpr (V >= PER) {
-        if (wide_out) {
-            if (e0 < E) {
-                char* p = static_cast<char*>(dl) + (row + e0) * (AT == A_F32 ? 4 : 2);
+    constexpr int N = Piece<AT>::N;
+    if constexpr (V >= N) {
 #pragma unroll
-                for (int c = 0; c < V / PER; ++c) {
-                    uint32_t u[4];
+        for (int c = 0; c < V; c += N) {
+            Piece<AT> p;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (AT == A_F32) u[i] = __float_as_uint(d[c * 4 + i]);
-                        else u[i] = round_bf16(d[c * 8 + 2 * i]) | (uint32_t)round_bf16(d[c * 8 + 2 * i + 1]) << 16;
-                    }
-                    reinterpret_cast<uint4*>(p)[c] = make_uint4(u[0], u[1], u[2], u[3]);
-                }
-            }
-            return;
+            for (int j = 0; j < N; ++j) p.v[j] = d[c + j];
+            const int left = E - e0 - c;
+            if (left >= N) p.template store<true, false>(dl, (int64_t)(row + e0 + c), N);
+            else p.template store<false, false>(dl, (int64_t)(row + e0 + c), left);
         }
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (e0 + j < E) store_one<AT>(dl, row + e0 + j, d[j]);
-}
-
-// 16-byte accesses: every lane's V values start on 16 bytes and lie inside the row.
-bool is_wide(const void* p, int64_t stride, int esize, int V, int E) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * esize % 16 == 0 && V * esize % 16 == 0 && E % V == 0;
+        for (int j = 0; j < V; ++j)
+            if (e0 + j < E) store_one<AT>(dl, row + e0 + j, d[j]);
+    }
 }
 
 // The least of V, 2V, .. 64 keys per lane that `lanes` lanes hold E keys with.
@@ -320,7 +315,7 @@ hipError_t route(const void* logits, int64_t stride, int T, int E, int K, int32_
         constexpr int L = decltype(lanes)::value, V = decltype(v)::value;
         constexpr int tokens = kTokensPerBlock * 64 / L;
         hipLaunchKernelGGL((k_route<AT, L, V, RENORM>), dim3((T + tokens - 1) / tokens), dim3(64 * kTokensPerBlock), 0, s,
-                           logits, stride, T, E, K, is_wide(logits, stride, AT == A_F32 ? 4 : 2, V, E), ids, w);
+                           logits, stride, T, E, K, ids, w);
         return hipGetLastError();
     };
     if (E > 512) return by_width<16>(64, E, [&](auto v) { return run(std::integral_constant<int, 64>{}, v); });
@@ -335,10 +330,9 @@ hipError_t route_backward(const void* logits, int64_t stride, const int32_t* ids
                           int E, int K, void* dl, int64_t dstride, hipStream_t s) {
     return by_width<1>(64, E, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        constexpr int es = AT == A_F32 ? 4 : 2;
         hipLaunchKernelGGL((k_route_backward<AT, V, RENORM>), dim3((T + kTokensPerBlock - 1) / kTokensPerBlock),
                            dim3(64 * kTokensPerBlock), kTokensPerBlock * 64 * V * sizeof(float), s, logits, stride, ids,
-                           w, dw, T, E, K, is_wide(logits, stride, es, V, E), is_wide(dl, dstride, es, V, E), dl, dstride);
+                           w, dw, T, E, K, dl, dstride);
         return hipGetLastError();
     });
 }

@@ -43,17 +43,6 @@ size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2; }
 // again (sorting 4096 x 8 rows of 4096 to e4m3 35.7 us, 44.7 with plain stores; combining
 // 4001 x 8 rows of 2048, bf16, 40.2 us against 44.2).  A small call's rows stay for the next kernel.
 constexpr int64_t kStream = (int64_t)32 << 20;
-typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint4 load_once(const void* p) {
-    const u32x4_t v = __builtin_nontemporal_load(static_cast<const u32x4_t*>(p));
-    return make_uint4(v.x, v.y, v.z, v.w);
-}
-template <bool STREAM>
-__device__ __forceinline__ void store16(void* p, uint4 q) {
-    const u32x4_t v = {q.x, q.y, q.z, q.w};
-    if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<u32x4_t*>(p));
-    else *static_cast<u32x4_t*>(p) = v;
-}
 
 // Exclusive prefix sums of v[0 .. E) in place, by the whole workgroup; returns the sum.
 __device__ int block_scan(int32_t* v, int E) {
@@ -139,33 +128,25 @@ __device__ __forceinline__ void waves_turn(int32_t* base, uint16_t* cnt, int E, 
 }
 
 // ---- a token's row to its K places -----------------------------------------------------
-// bx lanes side by side (a power of two) walk the row; rows: the token's K places.
-// Copies: 16-byte pieces when `wide`, else one element at a time.
+// bx lanes side by side, of all the workgroups that share the row, walk it from piece c on;
+// rows: the token's K places.
 template <int AT, bool STREAM>
-__device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, bool wide, const int32_t* rows, int K,
-                                         void* out, int c, int bx) {
-    constexpr int es = AT == A_F32 ? 4 : 2;
-    if (wide) {
-        const char* src = static_cast<const char*>(x) + row * es;
-        const int n = H * es / 16;
-        for (; c < n; c += bx) {
-            const uint4 q = reinterpret_cast<const uint4*>(src)[c];
-            for (int k = 0; k < K; ++k) {
-                const int r = rows[k];
-                if (r >= 0) store16<STREAM>(static_cast<char*>(out) + ((int64_t)r * H * es + (int64_t)c * 16), q);
-            }
-        }
-        return;
-    }
-    for (; c < H; c += bx) {
-        if constexpr (AT == A_F32) {
-            const float v = static_cast<const float*>(x)[row + c];
+__device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, const int32_t* rows, int K, void* out, int c,
+                                         int bx) {
+    using V = Piece<AT>;
+    typedef typename Bits<AT>::one One;
+    const One* src = static_cast<const One*>(x) + row;
+    One* dst = static_cast<One*>(out);
+    for (; c * V::N < H; c += bx) {
+        const int e = c * V::N;
+        if (e + V::N <= H) {
+            const u32x4_t q = load16<AT>(src + e, true);
             for (int k = 0; k < K; ++k)
-                if (rows[k] >= 0) static_cast<float*>(out)[(int64_t)rows[k] * H + c] = v;
+                if (rows[k] >= 0) store16<AT, STREAM>(dst + ((int64_t)rows[k] * H + e), q);
         } else {
-            const uint16_t v = static_cast<const uint16_t*>(x)[row + c];
-            for (int k = 0; k < K; ++k)
-                if (rows[k] >= 0) static_cast<uint16_t*>(out)[(int64_t)rows[k] * H + c] = v;
+            for (int i = e; i < H; ++i)
+                for (int k = 0; k < K; ++k)
+                    if (rows[k] >= 0) dst[(int64_t)rows[k] * H + i] = src[i];
         }
     }
 }
@@ -173,44 +154,23 @@ __device__ __forceinline__ void copy_row(const void* x, int64_t row, int H, bool
 // e4m3: a lane takes 16 values, eight lanes side by side a block of 128 (bx is a multiple
 // of 8, H of 16; a last block may be shorter).
 template <int AT, bool STREAM>
-__device__ __forceinline__ void round_row(const void* x, int64_t row, int H, bool wide, const int32_t* rows, int K,
-                                          uint8_t* out, float* scales, int c, int bx) {
+__device__ __forceinline__ void round_row(const void* x, int64_t row, int H, const int32_t* rows, int K, uint8_t* out,
+                                          float* scales, int c, int bx) {
+    using V = Piece<AT>;
     const int n = H / 16, nb = (H + kBlock - 1) / kBlock;
-    const int steps = (n + bx - 1) / bx;   // every lane takes part in every step's exchange
+    const int steps = (n - c / 8 * 8 + bx - 1) / bx;   // eight lanes take part in each step's exchange
     for (int s = 0; s < steps; ++s, c += bx) {
         float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
         if (c < n) {
-            if (wide) {
-                if constexpr (AT == A_F32) {
-                    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(x) + row) + c * 4;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 q = p[i];
-                        v[4 * i] = __uint_as_float(q.x);
-                        v[4 * i + 1] = __uint_as_float(q.y);
-                        v[4 * i + 2] = __uint_as_float(q.z);
-                        v[4 * i + 3] = __uint_as_float(q.w);
-                    }
-                } else {
-                    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + row) + c * 2;
+            for (int i = 0; i < 16 / V::N; ++i) {
+                V p;
+                p.template load<true>(x, row + (int64_t)c * 16 + i * V::N, V::N, true);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 q = p[i];
-                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            v[8 * i + 2 * j] = widen_bf16((uint16_t)u[j]);
-                            v[8 * i + 2 * j + 1] = widen_bf16((uint16_t)(u[j] >> 16));
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = load_one<AT>(x, (size_t)row + (size_t)c * 16 + i);
+                for (int j = 0; j < V::N; ++j) v[i * V::N + j] = p.v[j];
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 0.0f;
         }
         float big = 0.0f;   // of the finite values: a NaN or an infinity poisons its own code alone
 #pragma unroll
@@ -224,15 +184,13 @@ __device__ __forceinline__ void round_row(const void* x, int64_t row, int H, boo
         big = fmaxf(big, __shfl_xor(big, 4));
         if (c >= n) continue;
         const float scale = f8_scale(big), inv = f8_inverse(scale);
-        uint4 q;
-        q.x = f8_pack(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-        q.y = f8_pack(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-        q.z = f8_pack(v[8] * inv, v[9] * inv, v[10] * inv, v[11] * inv);
-        q.w = f8_pack(v[12] * inv, v[13] * inv, v[14] * inv, v[15] * inv);
+        u32x4_t q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = f8_pack(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
         for (int k = 0; k < K; ++k) {
             const int64_t r = rows[k];
             if (r < 0) continue;
-            store16<STREAM>(out + r * H + (int64_t)c * 16, q);
+            store16<A_F32, STREAM>(out + r * H + (int64_t)c * 16, q);   // on 16 bytes
             if ((c & 7) == 0) scales[r * nb + (c >> 3)] = scale;
         }
     }
@@ -242,15 +200,14 @@ struct Spread {
     const void* x;
     int64_t stride;
     int T, K, H, bx;
-    bool wide;
     void* out;
     float* scales;
 };
 
 template <int AT, bool F8, bool STREAM>
 __device__ __forceinline__ void spread_token(const Spread& a, int64_t t, const int32_t* rows, int c) {
-    if constexpr (F8) round_row<AT, STREAM>(a.x, t * a.stride, a.H, a.wide, rows, a.K, static_cast<uint8_t*>(a.out), a.scales, c, a.bx);
-    else copy_row<AT, STREAM>(a.x, t * a.stride, a.H, a.wide, rows, a.K, a.out, c, a.bx);
+    if constexpr (F8) round_row<AT, STREAM>(a.x, t * a.stride, a.H, rows, a.K, static_cast<uint8_t*>(a.out), a.scales, c, a.bx * gridDim.y);
+    else copy_row<AT, STREAM>(a.x, t * a.stride, a.H, rows, a.K, a.out, c, a.bx * gridDim.y);
 }
 
 // At most kOneLaunch pairs: every workgroup sorts them all (a few microseconds of ballots,
@@ -278,10 +235,10 @@ __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* 
         if (p < P) {
             const int v = id[r] >= 0 ? base[id[r]] + cnt[wave * E + id[r]] + rank[r] : -1;
             place[p] = v;
-            if (blockIdx.x == 0) rows[p] = v;
+            if (blockIdx.x == 0 && blockIdx.y == 0) rows[p] = v;
         }
     }
-    if (blockIdx.x == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
         for (int e = threadIdx.x; e < E; e += kThreads) offsets[e] = base[e];
         if (threadIdx.x == 0) offsets[E] = all;
     }
@@ -289,7 +246,7 @@ __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* 
     if (!a.x) return;
     const int by = kThreads / a.bx;
     const int t = blockIdx.x * by + threadIdx.x / a.bx;
-    if (t < a.T) spread_token<AT, F8, false>(a, t, place + t * a.K, threadIdx.x & (a.bx - 1));
+    if (t < a.T) spread_token<AT, F8, false>(a, t, place + t * a.K, blockIdx.y * a.bx + (threadIdx.x & (a.bx - 1)));
 }
 
 // More pairs: counts per workgroup, then places, then the rows (a launch each).
@@ -373,46 +330,15 @@ __global__ __launch_bounds__(kThreads) void k_spread(Spread a, const int32_t* __
     const int by = kThreads / a.bx;
     int64_t t = (int64_t)blockIdx.x * by + threadIdx.x / a.bx;
     if (a.bx >= 64) t = __builtin_amdgcn_readfirstlane((int)t);   // one token per wave: its places are scalars
-    if (t < a.T) spread_token<AT, F8, STREAM>(a, t, rows + t * a.K, threadIdx.x & (a.bx - 1));
+    if (t < a.T) spread_token<AT, F8, STREAM>(a, t, rows + t * a.K, blockIdx.y * a.bx + (threadIdx.x & (a.bx - 1)));
 }
 
 // ---- back: the weighted sum -------------------------------------------------------------
-template <int AT, bool WIDE>
-struct Piece {
-    static constexpr int N = WIDE ? (AT == A_F32 ? 4 : 8) : 1;
-    float v[N];
-    __device__ __forceinline__ void load(const void* p, int64_t i, bool once) {   // i: element index
-        if constexpr (WIDE) {
-            const char* at = static_cast<const char*>(p) + i * (AT == A_F32 ? 4 : 2);
-            const uint4 q = once ? load_once(at) : *reinterpret_cast<const uint4*>(at);
-            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = AT == A_F32 ? __uint_as_float(u[j & 3]) : widen_bf16((uint16_t)(u[j >> 1] >> (16 * (j & 1))));
-        } else {
-            v[0] = load_one<AT>(p, (size_t)i);
-        }
-    }
-    template <bool STREAM>
-    __device__ __forceinline__ void store(void* p, int64_t i) const {
-        if constexpr (WIDE) {
-            uint32_t u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (AT == A_F32) u[j] = __float_as_uint(v[j]);
-                else u[j] = round_bf16(v[2 * j]) | (uint32_t)round_bf16(v[2 * j + 1]) << 16;
-            }
-            store16<STREAM>(static_cast<char*>(p) + i * (AT == A_F32 ? 4 : 2), make_uint4(u[0], u[1], u[2], u[3]));
-        } else {
-            store_one<AT>(p, (size_t)i, v[0]);
-        }
-    }
-};
-
-template <int AT, bool WIDE, bool STREAM>
+template <int AT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restrict__ ys, const int32_t* __restrict__ rows,
         const float* __restrict__ w, const void* __restrict__ resid, int T, int K, int H, int bx,
         void* __restrict__ out) {
-    using V = Piece<AT, WIDE>;
+    using V = Piece<AT>;
     constexpr int KU = 8;   // rows in flight per lane
     const int by = kThreads / bx;
     int t = blockIdx.x * by + threadIdx.x / bx;
@@ -420,48 +346,58 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restric
     const int c = (blockIdx.y * bx + (threadIdx.x & (bx - 1))) * V::N;
     if (t >= T || c >= H) return;
     const unsigned P = (unsigned)T * (unsigned)K;
-    V acc;
+    auto piece = [&](auto whole) {
+        constexpr bool FULL = decltype(whole)::value;
+        const int left = H - c;
+        V acc;
 #pragma unroll
-    for (int i = 0; i < V::N; ++i) acc.v[i] = 0.0f;
-    for (int k0 = 0; k0 < K; k0 += KU) {
-        V y[KU];
-        bool on[KU];
-        float wk[KU];
+        for (int i = 0; i < V::N; ++i) acc.v[i] = 0.0f;
+        for (int k0 = 0; k0 < K; k0 += KU) {
+            V y[KU];
+            bool on[KU];
+            float wk[KU];
 #pragma unroll
-        for (int j = 0; j < KU; ++j) {
-            const int k = k0 + j;
-            const int r = k < K ? rows[(int64_t)t * K + k] : -1;
-            on[j] = (unsigned)r < P;   // any other place: a pair that went to no expert
-            wk[j] = on[j] && w ? w[(int64_t)t * K + k] : 1.0f;
-            if (on[j]) y[j].load(ys, (int64_t)r * H + c, true);
+            for (int j = 0; j < KU; ++j) {
+                const int k = k0 + j;
+                const int r = k < K ? rows[(int64_t)t * K + k] : -1;
+                on[j] = (unsigned)r < P;   // any other place: a pair that went to no expert
+                wk[j] = on[j] && w ? w[(int64_t)t * K + k] : 1.0f;
+                if (on[j]) y[j].template load<FULL>(ys, (int64_t)r * H + c, left, true);
+            }
+#pragma unroll
+            for (int j = 0; j < KU; ++j)
+                if (on[j])
+#pragma unroll
+                    for (int i = 0; i < V::N; ++i) acc.v[i] += wk[j] * y[j].v[i];
         }
+        if (resid) {
+            V r;
+            r.template load<FULL>(resid, (int64_t)t * H + c, left, true);
 #pragma unroll
-        for (int j = 0; j < KU; ++j)
-            if (on[j])
-#pragma unroll
-                for (int i = 0; i < V::N; ++i) acc.v[i] += wk[j] * y[j].v[i];
-    }
-    if (resid) {
-        V r;
-        r.load(resid, (int64_t)t * H + c, true);
-#pragma unroll
-        for (int i = 0; i < V::N; ++i) acc.v[i] += r.v[i];
-    }
-    acc.template store<STREAM>(out, (int64_t)t * H + c);
+            for (int i = 0; i < V::N; ++i) acc.v[i] += r.v[i];
+        }
+        acc.template store<FULL, STREAM>(out, (int64_t)t * H + c, left);
+    };
+    if (c + V::N <= H) piece(std::true_type{});
+    else piece(std::false_type{});
 }
 
-// A wave takes a token and up to eight of its pairs (grid.y walks the groups of pairs):
-// d_out[t] is read once for them, each pair's dot product stays in a register per lane and
-// is summed over the wave at the end, in a fixed order.
-template <int AT, bool WIDE, bool STREAM>
-__global__ __launch_bounds__(kThreads) void k_combine_rows_backward(const void* __restrict__ dout,
+// W waves take a token and up to eight of its pairs (grid.y walks the groups of pairs): d_out[t]
+// is read once for them, each pair's dot product stays in a register per lane and is summed
+// over the lanes, then the waves, at the end, in a fixed order.  One wave a token when there are
+// enough of them; few tokens are split over more (one token, 12 pairs, 8192 values, fp32:
+// 8.5 us, 35 with one wave).
+template <int AT, bool STREAM, int W>
+__global__ __launch_bounds__(W > kWaves ? 64 * W : kThreads) void k_combine_rows_backward(const void* __restrict__ dout,
         const void* __restrict__ ys, const int32_t* __restrict__ rows, const float* __restrict__ w, int T, int K, int per,
         int H, void* __restrict__ dys, float* __restrict__ dw) {
-    using V = Piece<AT, WIDE>;
+    using V = Piece<AT>;
     constexpr int KU = 8;
-    const int lane = threadIdx.x & 63;
-    const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + (threadIdx.x >> 6));
-    if (t >= T) return;
+    constexpr int TOKENS = W > kWaves ? 1 : kWaves / W;   // of a workgroup
+    __shared__ float sums[W > 1 ? W : 1][KU];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x * TOKENS + wave / W, part = wave % W;
+    if (t >= T) return;                                 // W > 1: one token a workgroup, which has one
     const int k0 = blockIdx.y * per, n = min(per, K - k0);
     const unsigned P = (unsigned)T * (unsigned)K;
     int64_t at[KU];
@@ -474,29 +410,46 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows_backward(const void* 
         wk[j] = at[j] >= 0 ? w[p] : 0.0f;
         dot[j] = 0.0f;
     }
-    for (int c = lane * V::N; c < H; c += 64 * V::N) {
-        V d, y[KU];
-        d.load(dout, (int64_t)t * H + c, false);
+    for (int c = (part * 64 + lane) * V::N; c < H; c += W * 64 * V::N) {
+        auto piece = [&](auto whole) {
+            constexpr bool FULL = decltype(whole)::value;
+            const int left = H - c;
+            V d, y[KU];
+            d.template load<FULL>(dout, (int64_t)t * H + c, left, false);
 #pragma unroll
-        for (int j = 0; j < KU; ++j)
-            if (at[j] >= 0) y[j].load(ys, at[j] + c, true);
+            for (int j = 0; j < KU; ++j)
+                if (at[j] >= 0) y[j].template load<FULL>(ys, at[j] + c, left, true);
 #pragma unroll
-        for (int j = 0; j < KU; ++j) {
-            if (at[j] < 0) continue;
-            V o;
+            for (int j = 0; j < KU; ++j) {
+                if (at[j] < 0) continue;
+                V o;
 #pragma unroll
-            for (int i = 0; i < V::N; ++i) {
-                dot[j] += y[j].v[i] * d.v[i];
-                o.v[i] = wk[j] * d.v[i];
+                for (int i = 0; i < V::N; ++i) {
+                    dot[j] += y[j].v[i] * d.v[i];
+                    o.v[i] = wk[j] * d.v[i];
+                }
+                o.template store<FULL, STREAM>(dys, at[j] + c, left);
             }
-            o.template store<STREAM>(dys, at[j] + c);
-        }
+        };
+        if (c + V::N <= H) piece(std::true_type{});
+        else piece(std::false_type{});
     }
 #pragma unroll
     for (int j = 0; j < KU; ++j) {
         if (j >= n) break;
         const float sum = wave_sum(dot[j]);
-        if (lane == 0) dw[(int64_t)t * K + k0 + j] = sum;
+        if (lane != 0) continue;
+        if constexpr (W == 1) dw[(int64_t)t * K + k0 + j] = sum;
+        else sums[part][j] = sum;
+    }
+    if constexpr (W > 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < n) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum += sums[i][threadIdx.x];
+            dw[(int64_t)t * K + k0 + threadIdx.x] = sum;
+        }
     }
 }
 
@@ -511,21 +464,23 @@ int lanes_for(int n, int lo) {
     while (bx < n && bx < kThreads) bx *= 2;
     return bx;
 }
-bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 template <int AT, bool F8>
 hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, int32_t* rows, int32_t* counts,
                 hipStream_t s) {
     Spread a = a0;
     constexpr int es = AT == A_F32 ? 4 : 2;
-    a.wide = on16(a.x) && a.stride * es % 16 == 0 && (F8 || (on16(a.out) && (int64_t)a.H * es % 16 == 0));
-    a.bx = F8 ? lanes_for(a.H / 16, 8) : lanes_for(a.wide ? a.H * es / 16 : a.H, 8);
+    const int pieces = F8 ? a.H / 16 : (a.H + Piece<AT>::N - 1) / Piece<AT>::N;
+    a.bx = lanes_for(pieces, 8);
     const int64_t P = (int64_t)a.T * a.K;
     const int bits = bits_of(E);
     const int by = kThreads / a.bx;
     const int tokens_grid = (a.T + by - 1) / by;
+    // few tokens: a row's pieces go over several workgroups
+    const int columns = tokens_grid < 512 ? (pieces + a.bx - 1) / a.bx : 1;
+    const dim3 grid(tokens_grid, columns);
     if (P <= kOneLaunch) {
-        hipLaunchKernelGGL((k_sort_one<AT, F8>), dim3(a.x ? tokens_grid : 1), dim3(kThreads), sort_lds(E), s, a, ids, E,
+        hipLaunchKernelGGL((k_sort_one<AT, F8>), a.x ? grid : dim3(1), dim3(kThreads), sort_lds(E), s, a, ids, E,
                            bits, offsets, rows);
         return hipGetLastError();
     }
@@ -536,44 +491,38 @@ hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, i
                        rows);
     if (!a.x) return hipGetLastError();
     if (P * a.H * (F8 ? 1 : es) > kStream)
-        hipLaunchKernelGGL((k_spread<AT, F8, true>), dim3(tokens_grid), dim3(kThreads), 0, s, a, rows);
+        hipLaunchKernelGGL((k_spread<AT, F8, true>), grid, dim3(kThreads), 0, s, a, rows);
     else
-        hipLaunchKernelGGL((k_spread<AT, F8, false>), dim3(tokens_grid), dim3(kThreads), 0, s, a, rows);
+        hipLaunchKernelGGL((k_spread<AT, F8, false>), grid, dim3(kThreads), 0, s, a, rows);
     return hipGetLastError();
 }
 
-template <int AT, bool WIDE, bool STREAM>
+template <int AT, bool STREAM>
 hipError_t combine(const void* ys, const int32_t* rows, const float* w, const void* resid, int T, int K, int H,
                    void* out, hipStream_t s) {
-    const int n = H / Piece<AT, WIDE>::N;
+    const int n = (H + Piece<AT>::N - 1) / Piece<AT>::N;
     const int bx = lanes_for(n, 8), by = kThreads / bx;
-    hipLaunchKernelGGL((k_combine_rows<AT, WIDE, STREAM>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0,
-                       s, ys, rows, w, resid, T, K, H, bx, out);
+    hipLaunchKernelGGL((k_combine_rows<AT, STREAM>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0, s, ys,
+                       rows, w, resid, T, K, H, bx, out);
     return hipGetLastError();
 }
 
-template <int AT, bool WIDE, bool STREAM>
+template <int AT, bool STREAM>
 hipError_t combine_backward(const void* dout, const void* ys, const int32_t* rows, const float* w, int T, int K, int H,
                             void* dys, float* dw, hipStream_t s) {
     const int groups = (K + 7) / 8, per = (K + groups - 1) / groups;
-    hipLaunchKernelGGL((k_combine_rows_backward<AT, WIDE, STREAM>), dim3((T + kWaves - 1) / kWaves, groups),
-                       dim3(kThreads), 0, s, dout, ys, rows, w, T, K, per, H, dys, dw);
-    return hipGetLastError();
-}
-
-// Calls f<AT, WIDE, STREAM>: 16-byte pieces where rows and bases allow them, and large calls'
-// stores past the caches (single elements are too slow for that to matter).
-template <class F>
-hipError_t by_form(int atype, bool wide, bool stream, F f) {
-    using std::integral_constant;
-    using Yes = integral_constant<bool, true>;
-    using No = integral_constant<bool, false>;
-    if (atype == A_F32) {
-        const integral_constant<int, A_F32> at;
-        return !wide ? f(at, No{}, No{}) : stream ? f(at, Yes{}, Yes{}) : f(at, Yes{}, No{});
+    auto run = [&](auto waves) {
+        constexpr int W = decltype(waves)::value, tokens = W > kWaves ? 1 : kWaves / W;
+        hipLaunchKernelGGL((k_combine_rows_backward<AT, STREAM, W>), dim3((T + tokens - 1) / tokens, groups),
+                           dim3(W > kWaves ? 64 * W : kThreads), 0, s, dout, ys, rows, w, T, K, per, H, dys, dw);
+        return hipGetLastError();
+    };
+    const int64_t waves = (int64_t)T * groups;
+    if constexpr (!STREAM) {                            // few tokens' rows are no large call
+        if (waves < 256 && H > 64 * 4 * Piece<AT>::N) return run(std::integral_constant<int, 16>{});
+        if (waves < 2048 && H > 64 * Piece<AT>::N) return run(std::integral_constant<int, 4>{});
     }
-    const integral_constant<int, A_BF16> at;
-    return !wide ? f(at, No{}, No{}) : stream ? f(at, Yes{}, Yes{}) : f(at, Yes{}, No{});
+    return run(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
@@ -588,7 +537,7 @@ size_t sort_workspace(int T, int K, int E) {
 hipError_t launch_sort(int atype, const void* x, int64_t stride, const int32_t* ids, int T, int K, int E, int H,
                        bool f8, void* sorted, float* scales, int32_t* offsets, int32_t* rows, void* workspace,
                        hipStream_t s) {
-    const Spread a{x, stride, T, K, H, 0, false, sorted, scales};
+    const Spread a{x, stride, T, K, H, 0, sorted, scales};
     int32_t* counts = static_cast<int32_t*>(workspace);
     if (atype == A_F32)
         return f8 ? sort<A_F32, true>(a, ids, E, offsets, rows, counts, s) : sort<A_F32, false>(a, ids, E, offsets, rows, counts, s);
@@ -597,21 +546,22 @@ hipError_t launch_sort(int atype, const void* x, int64_t stride, const int32_t* 
 
 hipError_t launch_combine(int atype, const void* ys, const int32_t* rows, const float* w, const void* resid, int T,
                           int K, int H, void* out, hipStream_t s) {
-    const int es = atype == A_F32 ? 4 : 2;
-    const bool wide = (int64_t)H * es % 16 == 0 && on16(ys) && on16(out) && (!resid || on16(resid));
-    return by_form(atype, wide, (int64_t)T * K * H * es > kStream, [&](auto at, auto wd, auto st) {
-        return combine<decltype(at)::value, decltype(wd)::value, decltype(st)::value>(ys, rows, w, resid, T, K, H, out, s);
-    });
+    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kStream;
+    if (atype == A_F32)
+        return stream ? combine<A_F32, true>(ys, rows, w, resid, T, K, H, out, s)
+                      : combine<A_F32, false>(ys, rows, w, resid, T, K, H, out, s);
+    return stream ? combine<A_BF16, true>(ys, rows, w, resid, T, K, H, out, s)
+                  : combine<A_BF16, false>(ys, rows, w, resid, T, K, H, out, s);
 }
 
 hipError_t launch_combine_backward(int atype, const void* dout, const void* ys, const int32_t* rows, const float* w,
                                    int T, int K, int H, void* dys, float* dw, hipStream_t s) {
-    const int es = atype == A_F32 ? 4 : 2;
-    const bool wide = (int64_t)H * es % 16 == 0 && on16(dout) && on16(ys) && on16(dys);
-    return by_form(atype, wide, (int64_t)T * K * H * es > kStream, [&](auto at, auto wd, auto st) {
-        return combine_backward<decltype(at)::value, decltype(wd)::value, decltype(st)::value>(dout, ys, rows, w, T, K, H,
-                                                                                             dys, dw, s);
-    });
+    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kStream;
+    if (atype == A_F32)
+        return stream ? combine_backward<A_F32, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
+                      : combine_backward<A_F32, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
+    return stream ? combine_backward<A_BF16, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
+                  : combine_backward<A_BF16, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
 }
 
 }  // namespace moe

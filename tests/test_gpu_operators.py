@@ -144,7 +144,7 @@ def hidden_for(T, H, seed, kind):
 
 
 SORTS = [(1, 1, 1, 16), (1, 8, 64, 2048), (8, 8, 64, 144), (128, 8, 60, 48), (129, 8, 64, 256), (700, 3, 5, 1008),
-         (2000, 6, 512, 32), (3, 64, 4096, 16), (2100, 8, 64, 2048)]
+         (2000, 6, 512, 32), (3, 64, 4096, 16), (2100, 8, 64, 2048), (2, 5, 16, 12400)]
 
 
 @pytest.mark.parametrize("mode", ["bf16", "f32", "bf16->f8", "f32->f8"])
@@ -205,7 +205,7 @@ def test_sort_places_alone_and_long(T, K, E):
 # ---- and back ------------------------------------------------------------------------------
 
 COMBINES = [(1, 1, 1, 8), (1, 8, 64, 2048), (3, 7, 9, 77), (65, 10, 60, 264), (300, 8, 64, 2560), (5, 64, 128, 100),
-            (2, 3, 8, 9000), (1100, 8, 64, 2048)]
+            (2, 3, 8, 9000), (1100, 8, 64, 2048), (2100, 4, 16, 40)]
 
 
 @pytest.mark.parametrize("weights,resid", [(True, True), (True, False), (False, False)])
