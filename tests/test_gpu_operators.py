@@ -143,7 +143,7 @@ def hidden_for(T, H, seed, kind):
     return dev(x, kind)
 
 
-SORTS = [(1, 1, 1, 16), (1, 8, 64, 2048), (8, 8, 64, 144), (128, 8, 60, 48), (129, 8, 64, 256), (700, 3, 5, 1008),
+SORTS = [(1, 1, 1, 16), (1, 8, 64, 2048), (8, 8, 64, 144), (128, 8, 60, 48), (129, 8, 64, 256), (256, 8, 64, 64), (257, 8, 60, 80), (700, 3, 5, 1008),
          (2000, 6, 512, 32), (3, 64, 4096, 16), (2100, 8, 64, 2048), (2, 5, 16, 12400)]
 
 

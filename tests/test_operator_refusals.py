@@ -56,8 +56,8 @@ def test_sort_refuses(change):
 
 def test_sort_workspace_bytes():
     f = binding.sort_workspace_bytes
-    assert f(1, 8, 64) == 0 and f(128, 8, 64) == 0
-    assert f(129, 8, 64) == 2 * 64 * 4            # two workgroups' counts
+    assert f(1, 8, 64) == 0 and f(256, 8, 64) == 0
+    assert f(257, 8, 64) == 3 * 64 * 4            # three workgroups' counts
     assert f(1 << 20, 16, 64) == 256 * 64 * 4     # never more than 256 of them
     assert f(-1, 8, 64) == 0 and f(8, 0, 64) == 0 and f(8, 8, 5000) == 0
 
