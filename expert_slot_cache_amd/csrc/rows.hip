@@ -13,6 +13,7 @@
 // Everything else moves rows: a token is read once for all of its K copies.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "ops.hpp"
@@ -28,6 +29,7 @@ constexpr int kPass = kThreads * kRounds;          // pairs a workgroup ranks at
 constexpr int kMaxBlocks = 256;                    // workgroups of the two-launch sort
 // Pairs up to which every workgroup of the one launch sorts them all for itself.
 constexpr int kOneLaunch = 2 * kPass;
+constexpr int kSorters = 512;                      // workgroups of that launch: two per CU hold
 
 // Pairs per workgroup of the two-launch sort (whole passes, at most kMaxBlocks workgroups).
 __host__ __device__ inline int64_t sort_chunk(int64_t P) {
@@ -239,9 +241,12 @@ __device__ __forceinline__ void spread_token(const Spread& a, int64_t t, const i
 }
 
 // At most kOneLaunch pairs: every workgroup sorts them all (a few microseconds, less than two
-// more launches and the waits for them: 200 x 8 rows of 4096 to e4m3 11.3 us, 18.4 in three launches), the first
-// writes rows and offsets, and each spreads its own tokens from the places it found.
-template <int AT, bool F8>
+// more launches and the waits for them), the first writes rows and offsets, and each spreads its
+// own tokens from the places it found.  No more than kSorters workgroups, so that all run at
+// once and none sorts after another has.  64 experts, against 2048 pairs and a token more in
+// three launches (us): 256 x 8 rows of 4096 to e4m3 11.4 / 12.7, 2048 x 1 of 1024 10.7 / 11.0, of
+// 4096 16.6 / 15.1; 256 x 8 of 16384, fp32, 34.7 / 36.1; 4096 experts: 20.8 / 28.2.
+template <int AT, bool F8, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* __restrict__ ids, int E, int bits,
         int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {
     extern __shared__ int32_t lds[];
@@ -261,8 +266,8 @@ __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* 
     });
     if (!a.x) return;
     const int by = kThreads / a.bx;
-    const int t = blockIdx.x * by + threadIdx.x / a.bx;
-    if (t < a.T) spread_token<AT, F8, false>(a, t, place + t * a.K, blockIdx.y * a.bx + (threadIdx.x & (a.bx - 1)));
+    for (int t = blockIdx.x * by + threadIdx.x / a.bx; t < a.T; t += gridDim.x * by)
+        spread_token<AT, F8, STREAM>(a, t, place + t * a.K, blockIdx.y * a.bx + (threadIdx.x & (a.bx - 1)));
 }
 
 // More pairs: counts per workgroup, then places, then the rows (a launch each).
@@ -462,19 +467,24 @@ hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, i
     const int tokens_grid = (a.T + by - 1) / by;
     // few tokens: a row's pieces go over several workgroups
     const int columns = tokens_grid < 512 ? (pieces + a.bx - 1) / a.bx : 1;
-    const dim3 grid(tokens_grid, columns);
+    const bool stream = P * a.H * (F8 ? 1 : es) > kStream;
     if (P <= kOneLaunch) {
-        hipLaunchKernelGGL((k_sort_one<AT, F8>), a.x ? grid : dim3(1), dim3(kThreads), sort_lds(E), s, a, ids, E,
-                           bits, offsets, rows);
+        const int across = std::min(columns, std::max(kSorters / std::max(tokens_grid, 1), 1));
+        const dim3 grid = a.x ? dim3(std::min(tokens_grid, kSorters), across) : dim3(1);
+        if (stream)
+            hipLaunchKernelGGL((k_sort_one<AT, F8, true>), grid, dim3(kThreads), sort_lds(E), s, a, ids, E, bits, offsets, rows);
+        else
+            hipLaunchKernelGGL((k_sort_one<AT, F8, false>), grid, dim3(kThreads), sort_lds(E), s, a, ids, E, bits, offsets, rows);
         return hipGetLastError();
     }
+    const dim3 grid(tokens_grid, columns);
     const int64_t chunk = sort_chunk(P);
     const int nb = (int)((P + chunk - 1) / chunk);
     hipLaunchKernelGGL(k_sort_count, dim3(nb), dim3(kThreads), (size_t)E * 4, s, ids, P, chunk, E, counts);
     hipLaunchKernelGGL(k_sort_place, dim3(nb), dim3(kThreads), sort_lds(E), s, ids, P, chunk, E, bits, counts, offsets,
                        rows);
     if (!a.x) return hipGetLastError();
-    if (P * a.H * (F8 ? 1 : es) > kStream)
+    if (stream)
         hipLaunchKernelGGL((k_spread<AT, F8, true>), grid, dim3(kThreads), 0, s, a, rows);
     else
         hipLaunchKernelGGL((k_spread<AT, F8, false>), grid, dim3(kThreads), 0, s, a, rows);

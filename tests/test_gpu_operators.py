@@ -144,7 +144,9 @@ def hidden_for(T, H, seed, kind):
 
 
 SORTS = [(1, 1, 1, 16), (1, 8, 64, 2048), (8, 8, 64, 144), (128, 8, 60, 48), (129, 8, 64, 256), (256, 8, 64, 64), (257, 8, 60, 80), (700, 3, 5, 1008),
-         (2000, 6, 512, 32), (3, 64, 4096, 16), (2100, 8, 64, 2048), (2, 5, 16, 12400)]
+         (2000, 6, 512, 32), (3, 64, 4096, 16), (2100, 8, 64, 2048), (2, 5, 16, 12400),
+         # one launch whose workgroups take several tokens each, one whose rows pass the caches too
+         (2000, 1, 5, 2064), (700, 2, 4096, 528), (1100, 1, 40, 16400)]
 
 
 @pytest.mark.parametrize("mode", ["bf16", "f32", "bf16->f8", "f32->f8"])
@@ -558,6 +560,63 @@ def test_binding_refuses_what_does_not_fit():
         with pytest.raises(binding.MoeError) as e:
             call()
         assert e.value.status == binding.EINVAL, i
+
+
+# ---- offsets past 32 bits ---------------------------------------------------------------------
+
+def test_rows_past_32_bits():
+    """Logits, tokens, sorted rows and their gradients whose elements number more than 2^32."""
+    T, H, E = (1 << 18) + 70, (1 << 14) + 16, 40
+    last = slice(T - 60, T)
+    lg = torch.empty(T * H, dtype=torch.bfloat16, device=DEV).as_strided((T, E), (H, 1))
+    z = logits_for(T, E, 3)
+    lg.copy_(dev(z, "bf16"))
+    ids, w = torch.empty((T, 1), dtype=torch.int32, device=DEV), torch.empty((T, 1), device=DEV)
+    binding.route(lg, ids, w, renorm=True)
+    assert np.array_equal(ids[last].cpu().numpy(), orows.route(host(lg[last]), 1, True)[0])
+    x = lg.as_strided((T, H), (H, 1))
+    x.fill_(1.0)
+    x[last] = hidden_for(60, H, 4, "bf16")
+    ids.fill_(3)
+    ids[: T // 2] = 2
+    off, rows = torch.empty(E + 1, dtype=torch.int32, device=DEV), torch.empty((T, 1), dtype=torch.int32, device=DEV)
+    out = torch.zeros((T, H), dtype=torch.bfloat16, device=DEV)
+    binding.sort_tokens(x, ids, out, off, rows)
+    assert torch.equal(rows[:, 0], torch.arange(T, dtype=torch.int32, device=DEV))    # in order already
+    assert torch.equal(out, x)
+    out.zero_()
+    binding.combine_rows(x, rows, out)
+    assert torch.equal(out, x)
+    out.zero_()
+    w.fill_(0.5)
+    d_w = torch.empty_like(w)
+    binding.combine_rows_backward(x, x, rows, w, out, d_w)
+    assert torch.equal(out[last], x[last] * 0.5) and (out[: T - 60] == 0.5).all()     # exact
+    size = (host(x[last]) ** 2).sum(1)
+    within(host(d_w[last, 0]), size, size * (H + 2) * U, "d_w")
+    codes, sc = torch.zeros((T, H), dtype=F8, device=DEV), torch.zeros((T, -(-H // 128)), device=DEV)
+    binding.sort_tokens(x, ids, codes, off, rows, scales=sc)
+    ref, ref_sc = orows.round_rows(host(x[last]))
+    assert np.array_equal(host(codes[last]), ref) and np.array_equal(host(sc[last]), ref_sc)
+
+
+@pytest.mark.parametrize("M,G,N,K", [((1 << 18) + 300, 2, 256, 1 << 14), (300, 70, 4096, 1 << 14), ((1 << 19) + 90, 2, 8448, 16)])
+def test_scaled_product_past_32_bits(M, G, N, K):
+    """Rows, matrices or outputs of more than 2^32 elements: the last group's last rows."""
+    kb, nb = -(-K // 128), -(-N // 128)
+    n = min(M // 2, 40)                                # rows of the last group that are looked at
+    x, w = torch.zeros((M, K), dtype=F8, device=DEV), torch.zeros((G, N, K), dtype=F8, device=DEV)
+    xs, ws = torch.ones((M, kb), device=DEV), torch.ones((G, nb, kb), device=DEV)
+    x[-n:], w[-1] = codes_for((n, K), 1).to(DEV), codes_for((N, K), 2).to(DEV)
+    xs[-n:], ws[-1] = dev(scales_for((n, kb), 3)), dev(scales_for((nb, kb), 4))
+    off = dev(np.array([0] + [M - n] * (G - 1) + [M], np.int32))
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    binding.scaled_product(x, xs, w, ws, out, offsets=off)
+    assert (out[: M - n] == 0).all()                   # rows of zeros
+    xv, wv = orows.widen_rows(host(x[-n:]), host(xs[-n:])), orows.widen_matrix(host(w[-1]), host(ws[-1]))
+    ref = xv @ wv.T
+    bound = np.abs(xv) @ np.abs(wv).T * (256 + 2 * kb + 6) * U + eights(xv) @ eights(wv).T * 2.0 ** -10
+    within(host(out[-n:]), ref, bound * (1 + HALF["bf16"]) + np.abs(ref) * HALF["bf16"], "out")
 
 
 def test_no_tokens():
