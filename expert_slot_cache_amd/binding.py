@@ -432,9 +432,12 @@ def _atype(torch, name: str, t) -> int:
     _bad(f"{name} is {t.dtype}, not float32 or bfloat16")
 
 
-def _matrix(name: str, t):
-    if t.dim() != 2:
-        _bad(f"{name} has {t.dim()} dimensions, not 2")
+def _matrix(name: str, t, dims: int = 2):
+    """The shape, every size of which the library's int32 holds."""
+    if t.dim() != dims:
+        _bad(f"{name} has {t.dim()} dimensions, not {dims}")
+    if max(t.shape) > 0x7fffffff:
+        _bad(f"{name} is {tuple(t.shape)}: sizes above 2^31 - 1")
     return t.shape
 
 
@@ -478,6 +481,8 @@ def route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, *, renorm: bool
 
 
 def sort_workspace_bytes(n_tokens: int, top_k: int, experts: int) -> int:
+    if max(n_tokens, top_k, experts) > 0x7fffffff:
+        return 0
     return int(lib().moe_sort_workspace_bytes(n_tokens, top_k, experts))
 
 
@@ -492,7 +497,7 @@ def sort_tokens(x, topk_ids, sorted_x, offsets, rows, *, scales=None, workspace=
     T, K = _matrix("topk_ids", topk_ids)
     _check_tensor("topk_ids", topk_ids, torch.int32, (T, K), dev)
     _check_tensor("rows", rows, torch.int32, (T, K), dev)
-    E = offsets.numel() - 1
+    E = min(offsets.numel() - 1, 0x7fffffff)
     _check_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     H = at = f8 = stride = 0
     if x is None:
@@ -564,9 +569,7 @@ def scaled_product(x, x_scales, w, w_scales, out, *, offsets=None, swiglu_scales
     import torch
     dev, s = _place(torch, stream)
     M, K = _matrix("x", x)
-    if w.dim() != 3:
-        _bad(f"w has {w.dim()} dimensions, not 3")
-    G, N, _ = w.shape
+    G, N, _ = _matrix("w", w, 3)
     f8, f32, kb = torch.float8_e4m3fn, torch.float32, -(-K // 128)
     _check_tensor("x", x, f8, (M, K), dev)
     _check_tensor("x_scales", x_scales, f32, (M, kb), dev)

@@ -14,7 +14,11 @@ void set_last_error(const char* msg);   // moe_pool.cpp
 
 namespace {
 
+// A launch has fewer than 2^32 lanes: 256 for each token, or 512 for 2^15 elements of a product
+// and the short last tiles of its groups.
 constexpr int64_t kMaxPairs = (int64_t)1 << 24;
+constexpr int32_t kMaxTokens = (1 << 24) - 1;
+constexpr int64_t kMaxElements = (int64_t)1 << 36;
 constexpr int32_t kMaxHidden = 1 << 17;
 
 moe_status_t fail(moe_status_t code, const char* fmt, ...) {
@@ -46,7 +50,7 @@ size_t act_size(int32_t atype) { return atype == MOE_A_F32 ? 4 : 2; }
 // The sizes every operator on (token, expert) pairs shares.
 moe_status_t check_pairs(int32_t atype, int32_t T, int32_t K) {
     CHECK(atype == MOE_A_F32 || atype == MOE_A_BF16, "atype %d invalid", atype);
-    CHECK(T >= 0, "n_tokens %d < 0", T);
+    CHECK(T >= 0 && T <= kMaxTokens, "n_tokens %d outside [0,%d]", T, kMaxTokens);
     CHECK(K >= 1 && K <= moe::kMaxTopK, "top_k %d outside [1,%d]", K, moe::kMaxTopK);
     CHECK((int64_t)T * K <= kMaxPairs, "n_tokens * top_k above %lld", (long long)kMaxPairs);
     return MOE_OK;
@@ -131,7 +135,7 @@ moe_status_t moe_sort_tokens(int32_t atype, const void* x_dev, int64_t x_stride,
     const size_t need = moe::sort_workspace(n_tokens, top_k, n_experts);
     CHECK(need == 0 || (!bad(workspace_dev, 4) && workspace_bytes >= need), "this sort needs %zu bytes of workspace", need);
     return launched(moe::launch_sort(atype, n_tokens ? x_dev : nullptr, x_stride, topk_ids_dev, n_tokens, top_k,
-                                     n_experts, hidden, to_fp8 != 0, sorted_dev, scales_dev, offsets_dev, rows_dev,
+                                     n_experts, x_dev ? hidden : 0, to_fp8 != 0, sorted_dev, scales_dev, offsets_dev, rows_dev,
                                      workspace_dev, static_cast<hipStream_t>(stream)),
                     "sort");
 }
@@ -175,6 +179,7 @@ moe_status_t moe_scaled_product(const void* x_dev, const float* x_scales_dev, co
     CHECK(n_groups == 1 || offsets_dev, "%d groups need offsets", n_groups);
     CHECK(aligned(offsets_dev, 4), "misaligned offsets");
     CHECK(n_cols >= 1 && n_cols <= 2 * kMaxHidden, "n_cols %d outside [1,%d]", n_cols, 2 * kMaxHidden);
+    CHECK((int64_t)n_rows * n_cols <= kMaxElements, "n_rows * n_cols above %lld", (long long)kMaxElements);
     CHECK(depth >= 16 && depth <= kMaxHidden && depth % 16 == 0, "depth %d: multiples of 16 up to %d", depth, kMaxHidden);
     CHECK(epilogue >= MOE_PRODUCT_F32 && epilogue <= MOE_PRODUCT_SWIGLU, "epilogue %d invalid", epilogue);
     const bool swiglu = epilogue == MOE_PRODUCT_SWIGLU;

@@ -52,8 +52,8 @@ __device__ __forceinline__ f32x4_t mfma_block(const Wide& a, const Wide& b) {
 
 // The work: the row tiles of all groups, TM rows each, times the column blocks of the matrix.
 // Every wave counts the tiles for itself: a lane takes a run of groups, a prefix over the lanes
-// orders the runs.  Offsets outside [0, M] or falling ones (they are device data) count as
-// empty groups, so that no row outside the buffers is ever touched.
+// orders the runs.  Offsets outside [0, M] or falling ones (they are device data) are
+// brought into [0, M], so that no row outside the buffers is ever touched.
 //
 // A group's work is listed up to four tiles at a time: those tiles of one column block, then
 // of the next.  Workgroups that run side by side on an XCD then read few different matrix and

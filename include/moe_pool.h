@@ -454,8 +454,8 @@ moe_status_t moe_forward_slots(int32_t wtype, int32_t atype, int32_t hidden, int
  * calls on different streams or in captured graphs are independent as long as their
  * buffers are, and a call with the same inputs gives the same bits.  Buffers are
  * contiguous but for the row strides (in elements) that are arguments, and do not
- * overlap.  Sizes: n_tokens * top_k <= 2^24 pairs, top_k <= 64, experts <= 4096, hidden
- * <= 2^17; n_tokens = 0 is accepted and (but for moe_sort_tokens' offsets) writes nothing. */
+ * overlap.  Sizes: n_tokens < 2^24, n_tokens * top_k <= 2^24 pairs, top_k <= 64, experts <=
+ * 4096, hidden <= 2^17; n_tokens = 0 is accepted and (but for moe_sort_tokens' offsets) writes nothing. */
 
 /* Top-k of a softmax router ("Running 125B MoE on Two 32 GB Cards", section 4.2: on a
  * tie of two logits the lower id wins).
@@ -532,13 +532,19 @@ moe_status_t moe_combine_rows_backward(int32_t atype, const void* d_out_dev, con
 /* e4m3 rows times their group's e4m3 matrix, with one scale for each 128 values of a row
  * and each 128 x 128 values of a matrix; group g has the rows offsets[g] .. offsets[g+1]:
  *   out[r][n] = sum_b xs[r][b] ws[g][n/128][b] sum_{k in block b} x[r][k] w[g][n][k]
- * (each block summed in fp32 by the matrix cores, the blocks added in fp32).
+ * The blocks are added in fp32, each times its two scales' product, which has to lie in
+ * fp32's range.  For F32 and SWIGLU a block is summed by the bf16 matrix
+ * instruction from the codes widened to bf16 (exact products, the sum within 2^-20 of the
+ * largest); for BF16 by the fp8 one, which drops what lies 13 bits below the largest of
+ * each eight products (a block's sum is off by less than 2^-10 of the sum of those
+ * largest ones, on normal inputs by far less than the rounding to bf16).
  *  x_dev         e4m3 [n_rows][depth], x_scales_dev float [n_rows][ceil(depth/128)].
  *  w_dev         e4m3 [n_groups][n_cols][depth], w_scales_dev float
  *                [n_groups][ceil(n_cols/128)][ceil(depth/128)].  depth: a multiple of 16; x_dev
- *                and w_dev on 16 bytes.
- *  offsets_dev   int32 [n_groups + 1], rising within [0, n_rows] (entries that are not count
- *                as empty groups), or NULL for one group of all n_rows rows.
+ *                and w_dev on 16 bytes; n_rows <= 2^24, n_rows * n_cols <= 2^36.
+ *  offsets_dev   int32 [n_groups + 1], rising within [0, n_rows], or NULL for one group of all n_rows
+ *                rows.  With others no memory outside the buffers is touched, but what out_dev
+ *                then holds is not defined.
  *  epilogue      MOE_PRODUCT_F32 / _BF16: out_dev [n_rows][n_cols] in that format.
  *                MOE_PRODUCT_SWIGLU (n_cols a multiple of 256): matrix rows [0, n_cols/2) are
  *                the gate, the rest the up projection; out_dev e4m3 [n_rows][n_cols/2] (on 16

@@ -67,7 +67,7 @@ COMBINE = dict(atype=BF16, ys=P, rows=P, w=P, resid=P, T=8, K=4, H=256, out=P, s
 
 @pytest.mark.parametrize("change", [
     dict(atype=3), dict(ys=None), dict(ys=P + 1), dict(rows=None), dict(w=P + 2), dict(resid=P + 1), dict(T=-2), dict(K=0),
-    dict(K=65), dict(H=0), dict(H=(1 << 17) + 1), dict(out=None), dict(out=P + 1)])
+    dict(K=65), dict(H=0), dict(H=(1 << 17) + 1), dict(T=1 << 24, K=1), dict(out=None), dict(out=P + 1)])
 def test_combine_refuses(change):
     _refused("moe_combine_rows", _with(COMBINE, **change))
 
@@ -87,7 +87,8 @@ PRODUCT = dict(x=P, xs=P, w=P, ws=P, offsets=P, M=8, G=4, N=256, K=128, ep=2, ou
 
 @pytest.mark.parametrize("change", [
     dict(x=None), dict(x=P + 8), dict(xs=None), dict(xs=P + 2), dict(w=None), dict(w=P + 8), dict(ws=None),
-    dict(offsets=None), dict(offsets=P + 2), dict(M=-1), dict(M=(1 << 24) + 1), dict(G=0), dict(G=4097), dict(N=0),
+    dict(offsets=None), dict(offsets=P + 2), dict(M=-1), dict(M=(1 << 24) + 1),
+    dict(M=1 << 23, N=(1 << 13) + 256), dict(G=0), dict(G=4097), dict(N=0),
     dict(N=128), dict(N=384), dict(K=0), dict(K=8), dict(K=120), dict(K=1 << 18), dict(ep=3), dict(ep=-1),
     dict(out=None), dict(out=P + 4), dict(os=None), dict(ep=0, out=P + 2), dict(ep=1, out=P + 1)])
 def test_scaled_product_refuses(change):
@@ -102,3 +103,13 @@ def test_scaled_product_refuses(change):
     ("moe_scaled_product", _with(PRODUCT, M=0, x=None, xs=None, w=None, ws=None, out=None, os=None))])
 def test_no_tokens_is_accepted_and_does_nothing(name, args):
     assert getattr(binding.lib(), name)(*args) == binding.OK
+
+
+def test_sizes_past_int32_are_refused_not_wrapped():
+    """A size is passed on as int32: 2^32 + 4 rows must not become four."""
+    torch = pytest.importorskip("torch")
+    big = torch.empty(1, dtype=torch.int32).expand((1 << 32) + 4, 1)
+    with pytest.raises(binding.MoeError, match="sizes above"):
+        binding._matrix("topk_ids", big)
+    assert tuple(binding._matrix("topk_ids", big[:4])) == (4, 1)
+    assert binding.sort_workspace_bytes((1 << 32) + 4000, 8, 64) == 0
