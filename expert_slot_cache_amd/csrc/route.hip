@@ -10,12 +10,13 @@
 //
 // Sixteen lanes (a DPP row) take a token up to 512 experts, a wave above that.  Lane i of them
 // holds the logits i*V .. i*V + V-1 as unsigned keys in float order, so that of equal keys the
-// lowest lane's lowest one is the lowest id.  The keys are put in order by eights; a round of
-// the selection is the maximum of the eights' heads over the lanes (DPP, no LDS), which the
-// first lane that holds it takes out of the first of its eights that does.  Softmax sums are
-// fp32.  A large call is bound by the instructions issued: 16384 tokens of 512 experts, top-10,
-// fp32, take 17 us (33.5 MB read); one token per wave and a search through its registers
-// took 22 us.
+// lowest lane's lowest one is the lowest id (a bf16 logit's key holds the id as well, and no two
+// are equal).  The keys are put in order by eights; a round of the selection is the maximum of
+// the eights' heads over the lanes (DPP, no LDS), which the first lane that holds it takes out of
+// the first of its eights that does.  Softmax sums are fp32.  A large call is bound by the
+// instructions issued: 16384 tokens of 512 experts, top-10, take 17.0 us in fp32 (33.5 MB read)
+// and 12.5 us in bf16; one token per wave and a search through its registers took 22 us in
+// fp32, exchanges of neighbours throughout, which keep equal keys in place, 17.9 and 16.8 us.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -28,7 +29,7 @@ namespace {
 
 constexpr int kTokensPerBlock = 4;   // waves per workgroup
 
-// Float order as unsigned order, every real key > 0 (0 marks a key that is absent or taken).
+// Float order as unsigned order, every real key > 0x7ffffe (less marks one that is absent or taken).
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t b = __float_as_uint(l);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
@@ -36,6 +37,9 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 __device__ __forceinline__ float logit_of(uint32_t k) {
     return __uint_as_float((k >> 31) ? k & 0x7fffffffu : ~k);
 }
+// A bf16 logit's key has its lower half to spare: the id, the lowest largest.  No two are equal.
+__device__ __forceinline__ uint32_t key_of(float l, int id) { return (key_of(l) & 0xffff0000u) | (uint32_t)(0xffff - id); }
+__device__ __forceinline__ float logit_of_id(uint32_t k) { return logit_of(k & 0x80000000u ? k & 0xffff0000u : k | 0xffffu); }
 // exp(l - m) for l <= m: the difference first, so that rows of any size keep in range (a whole
 // row of the type's lowest value is a uniform one), then 2^(d log2 e), within |d| 2^-23 of the
 // value.  With m infinite: equal logits count 1 each, the limit at +inf, and a row of -inf alone
@@ -74,52 +78,83 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-// A lane's V keys in eights, each in descending order with the places its keys had.
-template <int V>
+// A lane's V keys in eights, each in descending order, and (NAMES) the places its keys had.
+template <int V, bool NAMES>
 struct Eights {
     static constexpr int W = V < 8 ? V : 8, N = V / W;
     uint32_t key[V];
-    uint32_t names[N];   // four bits per key
-    // By exchanges of neighbours, which keep equal keys in place.
+    uint32_t names[NAMES ? N : 1];   // four bits per key
+    template <class F>
+    static __device__ __forceinline__ void exchange(uint32_t* k, uint32_t* name, int i, int j, F falls) {
+        // values, not elements: a choice between two elements becomes an address
+        const uint32_t a = k[i], b = k[j];
+        if constexpr (NAMES) {
+            const uint32_t an = name[i], bn = name[j];
+            const bool swap = falls(a, an, b, bn);
+            name[i] = swap ? bn : an;
+            name[j] = swap ? an : bn;
+            k[i] = swap ? b : a;
+            k[j] = swap ? a : b;
+        } else {
+            k[i] = max(a, b);
+            k[j] = min(a, b);
+        }
+    }
+    // By Batcher's merge exchange: 19 for eight keys; of four or two those whose sides exist.  That
+    // may turn equal keys round: where a wave has some, exchanges of neighbours put them right.
     __device__ __forceinline__ void order() {
+        constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                    {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+        uint32_t name[V];
+        bool equal = false;
+#pragma unroll
+        for (int j = 0; j < V; ++j) name[j] = j % W;
 #pragma unroll
         for (int g = 0; g < N; ++g) {
-            uint32_t* k = key + g * W;
-            uint32_t name[W];
 #pragma unroll
-            for (int j = 0; j < W; ++j) name[j] = j;
+            for (int i = 0; i < 19; ++i)
+                if (net[i][1] < W)
+                    exchange(key + g * W, name + g * W, net[i][0], net[i][1],
+                             [](uint32_t a, uint32_t, uint32_t b, uint32_t) { return a < b; });
 #pragma unroll
-            for (int r = 0; r < W; ++r)
+            for (int j = 0; j + 1 < W; ++j) equal |= key[g * W + j] == key[g * W + j + 1];
+        }
+        if constexpr (NAMES) {
+            if (__any(equal))
 #pragma unroll
-                for (int j = 0; j + 1 < W; ++j) {
-                    if ((j & 1) != (r & 1)) continue;
-                    // values, not elements: a choice between two elements becomes an address
-                    const uint32_t a = k[j], b = k[j + 1], an = name[j], bn = name[j + 1];
-                    k[j] = a < b ? b : a;
-                    k[j + 1] = a < b ? a : b;
-                    name[j] = a < b ? bn : an;
-                    name[j + 1] = a < b ? an : bn;
-                }
-            names[g] = 0;
+                for (int g = 0; g < N; ++g)
 #pragma unroll
-            for (int j = 0; j < W; ++j) names[g] |= name[j] << (4 * j);
+                    for (int r = 0; r < W; ++r)
+#pragma unroll
+                        for (int j = r & 1; j + 1 < W; j += 2)
+                            exchange(key + g * W, name + g * W, j, j + 1, [](uint32_t a, uint32_t an, uint32_t b, uint32_t bn) {
+                                return a == b && an > bn;
+                            });
+#pragma unroll
+            for (int g = 0; g < N; ++g) {
+                names[g] = 0;
+#pragma unroll
+                for (int j = 0; j < W; ++j) names[g] |= name[g * W + j] << (4 * j);
+            }
         }
     }
     __device__ __forceinline__ uint32_t best() const {
         uint32_t b = key[0];
 #pragma unroll
-        for (int g = 1; g < N; ++g) b = key[g * W] > b ? key[g * W] : b;
+        for (int g = 1; g < N; ++g) b = max(b, key[g * W]);
         return b;
     }
-    // Where `mine`: takes `top` out of the first of the eights that it heads; its place.
+    // Where `mine`: takes `top` out of the first of the eights that it heads; (NAMES) its place.
     __device__ __forceinline__ int take(uint32_t top, bool mine) {
         int at = 0;
 #pragma unroll
         for (int g = 0; g < N; ++g) {
             const bool hit = mine && key[g * W] == top;
-            mine = mine && !hit;
-            at = hit ? g * W + (int)(names[g] & 15) : at;
-            names[g] = hit ? names[g] >> 4 : names[g];
+            if constexpr (NAMES) {
+                mine = mine && !hit;
+                at = hit ? g * W + (int)(names[g] & 15) : at;
+                names[g] = hit ? names[g] >> 4 : names[g];
+            }
 #pragma unroll
             for (int j = 0; j < W; ++j) {
                 const uint32_t next = j + 1 < W ? key[g * W + j + 1] : 0u;
@@ -195,23 +230,31 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route(const void* __re
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int sub = lane / L, l = lane % L;            // the wave's token, and the lane in it
     const int t = (blockIdx.x * kTokensPerBlock + wave) * PER + sub;
-    const bool here = t < T;                           // the wave's other lanes go through the motions
+    const bool here = t < T;                           // the wave's other lanes go through the motions,
+    const int n = here ? E : 0;                        // with no logits
     float logit[V], sum = 0.0f;
-    load_logits<AT, V>(logits, (size_t)(here ? t : 0) * (size_t)stride, here ? E : 0, l, logit);
+    load_logits<AT, V>(logits, (size_t)(here ? t : 0) * (size_t)stride, n, l, logit);
     const float m = softmax_sum<L, V>(logit, !RENORM, &sum);
-    Eights<V> keys;
+    constexpr bool NAMES = AT == A_F32;
+    Eights<V, NAMES> keys;
 #pragma unroll
-    for (int j = 0; j < V; ++j) keys.key[j] = l * V + j < E ? key_of(logit[j]) : 0u;
+    for (int j = 0; j < V; ++j) {
+        const int e = l * V + j;                       // absent keys: none equal
+        if constexpr (NAMES) keys.key[j] = e < n ? key_of(logit[j]) : (uint32_t)j;
+        else keys.key[j] = e < n ? key_of(logit[j], e) : (uint32_t)j;
+    }
     keys.order();
     const uint64_t below = L == 64 ? 0 : ((1ull << lane) - 1) & (0xffffull << (lane & 48));   // of this token's
     for (int k = 0; k < K; ++k) {
         const uint32_t best = keys.best(), top = lanes_max<L>(best);
-        const uint64_t holds = __ballot(best == top);
-        bool mine;
-        if constexpr (L == 64) mine = lane == __builtin_ctzll(holds);   // some lane holds top
-        else mine = best == top && (holds & below) == 0;
+        bool mine = best == top;
+        if constexpr (NAMES) {
+            const uint64_t holds = __ballot(mine);
+            if constexpr (L == 64) mine = lane == __builtin_ctzll(holds);   // some lane holds top
+            else mine = mine && (holds & below) == 0;
+        }
         const int at = keys.take(top, mine);
-        if (mine) found[wave][sub][k] = make_uint2((uint32_t)(l * V + at), top);
+        if (mine) found[wave][sub][k] = make_uint2(NAMES ? (uint32_t)(l * V + at) : 0xffff - (top & 0xffff), top);
     }
     __builtin_amdgcn_wave_barrier();                   // LDS operations of one wave complete in order
     const uint2* f = found[wave][sub];
@@ -220,7 +263,7 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route(const void* __re
 #pragma unroll
     for (int i = 0; i < kMaxTopK / L; ++i) {
         const int k = l + i * L;
-        mine[i] = k < K ? term(logit_of(f[k].y), m) : 0.0f;
+        mine[i] = k < K ? term(NAMES ? logit_of(f[k].y) : logit_of_id(f[k].y), m) : 0.0f;
         if constexpr (RENORM) sum += mine[i];
     }
     if constexpr (RENORM) sum = lanes_sum<L>(sum);
