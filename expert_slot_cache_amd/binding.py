@@ -399,11 +399,9 @@ def _bad(what: str):
     raise MoeError(EINVAL, what)
 
 
-def _check_tensor(name: str, t, dtype, shape, dev: int, rows: bool = False):
-    """t lies on device `dev`, is of this dtype and shape, and contiguous (`rows`: only
-    within its rows)."""
-    if t is not None and t.get_device() == dev and t.dtype is dtype and t.shape == shape and \
-            (t.is_contiguous() or rows and t.stride(1) == 1):
+def _check_tensor(name: str, t, dtype, shape, dev: int):
+    """t lies on device `dev`, is contiguous and of this dtype and shape."""
+    if t is not None and t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return
     if t is None:
         _bad(f"{name} is missing")
@@ -413,32 +411,49 @@ def _check_tensor(name: str, t, dtype, shape, dev: int, rows: bool = False):
         _bad(f"{name} is {t.dtype}, not {dtype}")
     if t.shape != shape:
         _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    if not rows:
-        _bad(f"{name} is not contiguous")
-    if shape[1] > 1:
+    _bad(f"{name} is not contiguous")
+
+
+def _sizes(name: str, t, dims: int):
+    """The shape of t, every size of which the library's int32 holds."""
+    if t is None:
+        _bad(f"{name} is missing")
+    shape = t.shape
+    if len(shape) != dims:
+        _bad(f"{name} has {len(shape)} dimensions, not {dims}")
+    for n in shape:
+        if n > 0x7fffffff:
+            _bad(f"{name} is {tuple(shape)}: sizes above 2^31 - 1")
+    return shape
+
+
+def _array(name: str, t, dtype, dev: int, dims: int = 2):
+    """The shape of a contiguous array of this dtype on device `dev`."""
+    shape = _sizes(name, t, dims)
+    if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+        _check_tensor(name, t, dtype, shape, dev)
+    return shape
+
+
+def _rows(name: str, t, dev: int):
+    """(rows, values of a row, elements from one row to the next) of a matrix on device `dev`
+    whose rows may be apart."""
+    n, h = _sizes(name, t, 2)
+    stride, one = t.stride()
+    if t.get_device() != dev:
+        _bad(f"{name} is not on the current device, cuda:{dev}")
+    if one != 1 and h > 1:
         _bad(f"the values of a row of {name} are not contiguous")
-
-
-def _stride(t) -> int:
-    """Elements from one row to the next."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return n, h, stride if n > 1 else h
 
 
 def _atype(torch, name: str, t) -> int:
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
         return A_BF16
-    if t.dtype is torch.float32:
+    if dtype is torch.float32:
         return A_F32
-    _bad(f"{name} is {t.dtype}, not float32 or bfloat16")
-
-
-def _matrix(name: str, t, dims: int = 2):
-    """The shape, every size of which the library's int32 holds."""
-    if t.dim() != dims:
-        _bad(f"{name} has {t.dim()} dimensions, not {dims}")
-    if max(t.shape) > 0x7fffffff:
-        _bad(f"{name} is {tuple(t.shape)}: sizes above 2^31 - 1")
-    return t.shape
+    _bad(f"{name} is {dtype}, not float32 or bfloat16")
 
 
 def _place(torch, stream):
@@ -452,12 +467,12 @@ def route(logits, topk_ids, topk_w, *, renorm: bool = True, stream=None):
     topk_w fp32 [T, K]; renorm: the weights of a token sum to one."""
     import torch
     dev, s = _place(torch, stream)
-    T, E = _matrix("logits", logits)
-    shape = (T, _matrix("topk_ids", topk_ids)[1])
-    _check_tensor("logits", logits, logits.dtype, logits.shape, dev, rows=True)
-    _check_tensor("topk_ids", topk_ids, torch.int32, shape, dev)
+    T, E, stride = _rows("logits", logits, dev)
+    shape = _array("topk_ids", topk_ids, torch.int32, dev)
+    if shape[0] != T:
+        _bad(f"topk_ids has {shape[0]} rows, logits {T}")
     _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
-    _check(lib().moe_route(_atype(torch, "logits", logits), logits.data_ptr(), _stride(logits), T, E, shape[1],
+    _check(lib().moe_route(_atype(torch, "logits", logits), logits.data_ptr(), stride, T, E, shape[1],
                            ROUTE_RENORM if renorm else ROUTE_SOFTMAX, topk_ids.data_ptr(), topk_w.data_ptr(), s))
 
 
@@ -466,18 +481,20 @@ def route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, *, renorm: bool
     route gave on these logits (with renorm they are not read and may be None)."""
     import torch
     dev, s = _place(torch, stream)
-    T, E = _matrix("d_logits", d_logits)
-    shape = (T, _matrix("topk_ids", topk_ids)[1])
-    _check_tensor("d_logits", d_logits, d_logits.dtype, d_logits.shape, dev, rows=True)
+    T, E, d_stride = _rows("d_logits", d_logits, dev)
+    stride = E
     if logits is not None:
-        _check_tensor("logits", logits, d_logits.dtype, d_logits.shape, dev, rows=True)
-    _check_tensor("topk_ids", topk_ids, torch.int32, shape, dev)
+        n, e, stride = _rows("logits", logits, dev)
+        if (n, e) != (T, E) or logits.dtype is not d_logits.dtype:
+            _bad(f"logits are {logits.dtype} {(n, e)}, d_logits {d_logits.dtype} {(T, E)}")
+    shape = _array("topk_ids", topk_ids, torch.int32, dev)
+    if shape[0] != T:
+        _bad(f"topk_ids has {shape[0]} rows, d_logits {T}")
     _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
     _check_tensor("d_topk_w", d_topk_w, torch.float32, shape, dev)
     _check(lib().moe_route_backward(_atype(torch, "d_logits", d_logits), _ptr(logits),
-                                    E if logits is None else _stride(logits), topk_ids.data_ptr(), topk_w.data_ptr(),
-                                    d_topk_w.data_ptr(), T, E, shape[1], ROUTE_RENORM if renorm else ROUTE_SOFTMAX,
-                                    d_logits.data_ptr(), _stride(d_logits), s))
+                                    stride, topk_ids.data_ptr(), topk_w.data_ptr(), d_topk_w.data_ptr(), T, E, shape[1],
+                                    ROUTE_RENORM if renorm else ROUTE_SOFTMAX, d_logits.data_ptr(), d_stride, s))
 
 
 def sort_workspace_bytes(n_tokens: int, top_k: int, experts: int) -> int:
@@ -494,9 +511,8 @@ def sort_tokens(x, topk_ids, sorted_x, offsets, rows, *, scales=None, workspace=
     allocator for this call (on torch's current stream only)."""
     import torch
     dev, s = _place(torch, stream)
-    T, K = _matrix("topk_ids", topk_ids)
-    _check_tensor("topk_ids", topk_ids, torch.int32, (T, K), dev)
-    _check_tensor("rows", rows, torch.int32, (T, K), dev)
+    shape = T, K = _array("topk_ids", topk_ids, torch.int32, dev)
+    _check_tensor("rows", rows, torch.int32, shape, dev)
     E = min(offsets.numel() - 1, 0x7fffffff)
     _check_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     H = at = f8 = stride = 0
@@ -504,9 +520,10 @@ def sort_tokens(x, topk_ids, sorted_x, offsets, rows, *, scales=None, workspace=
         if sorted_x is not None or scales is not None:
             _bad("sorted rows need x")
     else:
-        H = _matrix("x", x)[1]
-        at, stride = _atype(torch, "x", x), _stride(x)
-        _check_tensor("x", x, x.dtype, (T, H), dev, rows=True)
+        n, H, stride = _rows("x", x, dev)
+        if n != T:
+            _bad(f"x has {n} rows, topk_ids {T}")
+        at = _atype(torch, "x", x)
         f8 = int(scales is not None)
         _check_tensor("sorted_x", sorted_x, torch.float8_e4m3fn if f8 else x.dtype, (T * K, H), dev)
         if f8:
@@ -530,13 +547,13 @@ def combine_rows(ys, rows, out, *, topk_w=None, resid=None, stream=None):
     the gradient of sort_tokens."""
     import torch
     dev, s = _place(torch, stream)
-    T, K = _matrix("rows", rows)
-    H = _matrix("out", out)[1]
-    _check_tensor("rows", rows, torch.int32, (T, K), dev)
-    _check_tensor("out", out, out.dtype, (T, H), dev)
+    shape = T, K = _array("rows", rows, torch.int32, dev)
+    n, H = _array("out", out, out.dtype, dev)
+    if n != T:
+        _bad(f"out has {n} rows, rows {T}")
     _check_tensor("ys", ys, out.dtype, (T * K, H), dev)
     if topk_w is not None:
-        _check_tensor("topk_w", topk_w, torch.float32, (T, K), dev)
+        _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
     if resid is not None:
         _check_tensor("resid", resid, out.dtype, (T, H), dev)
     _check(lib().moe_combine_rows(_atype(torch, "out", out), ys.data_ptr(), rows.data_ptr(), _ptr(topk_w), _ptr(resid),
@@ -548,14 +565,14 @@ def combine_rows_backward(d_out, ys, rows, topk_w, d_ys, d_topk_w, *, stream=Non
     they are) and d_topk_w fp32 [T, K], for what combine_rows took."""
     import torch
     dev, s = _place(torch, stream)
-    T, K = _matrix("rows", rows)
-    H = _matrix("d_out", d_out)[1]
-    _check_tensor("rows", rows, torch.int32, (T, K), dev)
-    _check_tensor("d_out", d_out, d_out.dtype, (T, H), dev)
+    shape = T, K = _array("rows", rows, torch.int32, dev)
+    n, H = _array("d_out", d_out, d_out.dtype, dev)
+    if n != T:
+        _bad(f"d_out has {n} rows, rows {T}")
     _check_tensor("ys", ys, d_out.dtype, (T * K, H), dev)
     _check_tensor("d_ys", d_ys, d_out.dtype, (T * K, H), dev)
-    _check_tensor("topk_w", topk_w, torch.float32, (T, K), dev)
-    _check_tensor("d_topk_w", d_topk_w, torch.float32, (T, K), dev)
+    _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
+    _check_tensor("d_topk_w", d_topk_w, torch.float32, shape, dev)
     _check(lib().moe_combine_rows_backward(_atype(torch, "d_out", d_out), d_out.data_ptr(), ys.data_ptr(),
                                            rows.data_ptr(), topk_w.data_ptr(), T, K, H, d_ys.data_ptr(),
                                            d_topk_w.data_ptr(), s))
@@ -568,12 +585,13 @@ def scaled_product(x, x_scales, w, w_scales, out, *, offsets=None, swiglu_scales
     swiglu_scales fp32 [M, N/256]: out is float8_e4m3fn [M, N/2], silu(gate) * up rounded."""
     import torch
     dev, s = _place(torch, stream)
-    M, K = _matrix("x", x)
-    G, N, _ = _matrix("w", w, 3)
-    f8, f32, kb = torch.float8_e4m3fn, torch.float32, -(-K // 128)
-    _check_tensor("x", x, f8, (M, K), dev)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    M, K = _array("x", x, f8, dev)
+    G, N, depth = _array("w", w, f8, dev, 3)
+    if depth != K:
+        _bad(f"rows of w have {depth} values, of x {K}")
+    kb = -(-K // 128)
     _check_tensor("x_scales", x_scales, f32, (M, kb), dev)
-    _check_tensor("w", w, f8, (G, N, K), dev)
     _check_tensor("w_scales", w_scales, f32, (G, -(-N // 128), kb), dev)
     if offsets is not None:
         _check_tensor("offsets", offsets, torch.int32, (G + 1,), dev)

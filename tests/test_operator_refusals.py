@@ -110,6 +110,15 @@ def test_sizes_past_int32_are_refused_not_wrapped():
     torch = pytest.importorskip("torch")
     big = torch.empty(1, dtype=torch.int32).expand((1 << 32) + 4, 1)
     with pytest.raises(binding.MoeError, match="sizes above"):
-        binding._matrix("topk_ids", big)
-    assert tuple(binding._matrix("topk_ids", big[:4])) == (4, 1)
+        binding._array("topk_ids", big, torch.int32, -1)
+    with pytest.raises(binding.MoeError, match="sizes above"):
+        binding._rows("x", big, -1)
+    assert tuple(binding._array("topk_ids", big[:4].contiguous(), torch.int32, -1)) == (4, 1)
     assert binding.sort_workspace_bytes((1 << 32) + 4000, 8, 64) == 0
+
+
+def test_missing_tensors_are_refused():
+    for call in (lambda: binding._array("topk_ids", None, None, 0), lambda: binding._rows("x", None, 0),
+                 lambda: binding._check_tensor("rows", None, None, (1, 1), 0)):
+        with pytest.raises(binding.MoeError, match="is missing"):
+            call()
