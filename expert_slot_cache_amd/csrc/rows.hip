@@ -97,12 +97,13 @@ __device__ __forceinline__ void rank_pass(int E, int bits, uint16_t* cnt, const 
 #pragma unroll
     for (int r = 0; r < kRounds; ++r) {
         uint64_t same = __ballot(id[r] >= 0);
+        rank[r] = 0;
+        if (same == 0) continue;                           // few pairs: most rounds have none
         for (int b = 0; b < bits; ++b) {
             const bool one = (id[r] >> b) & 1;
             const uint64_t m = __ballot(one);
             same &= one ? m : ~m;
         }
-        rank[r] = 0;
         if (id[r] >= 0) {
             const int before = lanes_below(same);
             const int sofar = mine[id[r]];
@@ -114,24 +115,30 @@ __device__ __forceinline__ void rank_pass(int E, int bits, uint16_t* cnt, const 
     }
 }
 
-// Counts of the pairs p0 .. end by expert, added to h[E] (zeroed here; a barrier follows).
-__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int64_t p0, int64_t end, int E, int32_t* h) {
+// Counts of the pairs p0 .. end by expert in h[E] (zeroed here; a barrier follows), `id` holding
+// the first pass of them already.
+__device__ __forceinline__ void count_pairs(const int32_t* __restrict__ ids, int64_t p0, int64_t end, int E, int32_t* h,
+                                            const int id[kRounds]) {
     for (int e = threadIdx.x; e < E; e += kThreads) h[e] = 0;
     __syncthreads();
-    for (int64_t p = p0 + threadIdx.x; p < end; p += kThreads) {
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+        if (id[r] >= 0) atomicAdd(&h[id[r]], 1);           // counts: the order does not matter
+    for (int64_t p = p0 + kPass + threadIdx.x; p < end; p += kThreads) {
         const int v = ids[p];
-        if ((unsigned)v < (unsigned)E) atomicAdd(&h[v], 1);   // counts: the order does not matter
+        if ((unsigned)v < (unsigned)E) atomicAdd(&h[v], 1);
     }
     __syncthreads();
 }
-// The pairs p0 .. end in their order: put(p, the pair's row), base[e] being the next row of e.
+// The pairs p0 .. end in their order: put(p, the pair's row), base[e] being the next row of e and
+// `id` the first pass of them.
 template <class F>
 __device__ __forceinline__ void place_pairs(const int32_t* __restrict__ ids, int64_t p0, int64_t end, int E, int bits,
-                                            int32_t* base, uint16_t* cnt, F put) {
+                                            int32_t* base, uint16_t* cnt, int id[kRounds], F put) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t q0 = p0; q0 < end; q0 += kPass) {
-        int id[kRounds], rank[kRounds];
-        load_pass(ids, q0, end, E, id);
+        int rank[kRounds];
+        if (q0 > p0) load_pass(ids, q0, end, E, id);
         rank_pass(E, bits, cnt, id, rank);
         __syncthreads();
 #pragma unroll
@@ -254,13 +261,15 @@ __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* 
     int32_t* base = lds;
     const int P = a.T * a.K;
     const bool writes = blockIdx.x == 0 && blockIdx.y == 0;
-    count_pairs(ids, 0, P, E, base);
+    int id[kRounds];
+    load_pass(ids, 0, P, E, id);
+    count_pairs(ids, 0, P, E, base, id);
     const int all = block_scan(base, E);
     if (writes) {
         for (int e = threadIdx.x; e < E; e += kThreads) offsets[e] = base[e];
         if (threadIdx.x == 0) offsets[E] = all;
     }
-    place_pairs(ids, 0, P, E, bits, base, reinterpret_cast<uint16_t*>(lds + E), [&](int64_t p, int v) {
+    place_pairs(ids, 0, P, E, bits, base, reinterpret_cast<uint16_t*>(lds + E), id, [&](int64_t p, int v) {
         place[p] = v;
         if (writes) rows[p] = v;
     });
@@ -275,7 +284,10 @@ __global__ __launch_bounds__(kThreads) void k_sort_count(const int32_t* __restri
         int32_t* __restrict__ counts) {
     extern __shared__ int32_t lds[];
     const int64_t p0 = blockIdx.x * chunk;
-    count_pairs(ids, p0, p0 + chunk < P ? p0 + chunk : P, E, lds);
+    const int64_t end = p0 + chunk < P ? p0 + chunk : P;
+    int id[kRounds];
+    load_pass(ids, p0, end, E, id);
+    count_pairs(ids, p0, end, E, lds, id);
     for (int e = threadIdx.x; e < E; e += kThreads) counts[(int64_t)blockIdx.x * E + e] = lds[e];
 }
 
@@ -287,6 +299,8 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(const int32_t* __restri
     int32_t* before = reinterpret_cast<int32_t*>(cnt);   // [E], until cnt is used
     const int nb = gridDim.x, b = blockIdx.x;
     const int64_t p0 = b * chunk, end = p0 + chunk < P ? p0 + chunk : P;
+    int id[kRounds];
+    load_pass(ids, p0, end, E, id);
     for (int e = threadIdx.x; e < E; e += kThreads) {   // of all workgroups, and of those before this one
         int sum = 0, mine = 0;
         for (int i = 0; i < nb; i += 16) {
@@ -311,7 +325,7 @@ __global__ __launch_bounds__(kThreads) void k_sort_place(const int32_t* __restri
     }
     if (b == 0 && threadIdx.x == 0) offsets[E] = all;
     __syncthreads();
-    place_pairs(ids, p0, end, E, bits, base, cnt, [&](int64_t p, int v) { rows[p] = v; });
+    place_pairs(ids, p0, end, E, bits, base, cnt, id, [&](int64_t p, int v) { rows[p] = v; });
 }
 
 template <int AT, bool F8, bool STREAM>
