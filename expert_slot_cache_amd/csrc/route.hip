@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kTokensPerBlock = 4;   // waves per workgroup
 
-// Float order as unsigned order, every real key > 0x7ffffe (less marks one that is absent or taken).
+// Float order as unsigned order, every real key > 0x7f0000 (less marks one that is absent or taken).
 __device__ __forceinline__ uint32_t key_of(float l) {
     const uint32_t b = __float_as_uint(l);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
