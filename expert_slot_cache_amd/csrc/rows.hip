@@ -251,8 +251,8 @@ __device__ __forceinline__ void spread_token(const Spread& a, int64_t t, const i
 // more launches and the waits for them), the first writes rows and offsets, and each spreads its
 // own tokens from the places it found.  No more than kSorters workgroups, so that all run at
 // once and none sorts after another has.  64 experts, against 2048 pairs and a token more in
-// three launches (us): 256 x 8 rows of 4096 to e4m3 11.4 / 12.7, 2048 x 1 of 1024 10.7 / 11.0, of
-// 4096 16.6 / 15.1; 256 x 8 of 16384, fp32, 34.7 / 36.1; 4096 experts: 20.8 / 28.2.
+// three launches (us): 256 x 8 rows of 4096 to e4m3 11.3 / 12.7, 2048 x 1 of 1024 10.4 / 11.0, of
+// 4096 15.6 / 14.3; 256 x 8 of 16384, fp32, 33.9 / 34.9; 4096 experts, of 4096: 20.7 / 27.8.
 template <int AT, bool F8, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_sort_one(Spread a, const int32_t* __restrict__ ids, int E, int bits,
         int32_t* __restrict__ offsets, int32_t* __restrict__ rows) {

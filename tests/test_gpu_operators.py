@@ -84,6 +84,23 @@ def test_route(T, E, K, kind, renorm):
     within(host(w), ref_w, ref_w * (2 * span + E + 8) * U + 2.0 ** -126, "weights")
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,K", [(61, 7, 7), (200, 64, 20), (97, 130, 64), (150, 512, 10), (33, 1024, 64), (20, 4096, 64)])
+def test_route_of_many_equal_logits(T, E, K, kind):
+    """Logits of a few values, infinities, zeros and NaN among them: ascending ids at every tie."""
+    rng = np.random.default_rng(T)
+    few = np.array([-INF, -2.0, -0.0, 0.0, 1.0, 1.0, 3.0, np.nan], np.float32)
+    z = few[rng.integers(0, len(few), (T, E))]
+    z[::3] = few[rng.integers(0, 5, (len(z[::3]), E))]
+    lg = dev(z, kind)
+    ids, w = torch.full((T, K), -5, dtype=torch.int32, device=DEV), torch.full((T, K), 7.0, device=DEV)
+    binding.route(lg, ids, w, renorm=False)
+    ref_ids, ref_w = orows.route(host(lg), K, False)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    # as in test_route, the logits' differences being at most 5
+    within(host(w), ref_w, ref_w * (2 * 5 + E + 8) * U + 2.0 ** -126, "weights")
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("T,E,K", ROUTES)
@@ -478,6 +495,60 @@ def test_layer_replayed_from_a_graph_and_on_another_stream():
                 layer.run()
             side.synchronize()
             assert torch.equal(layer.out, eager)
+
+
+def test_layers_and_gradients_at_once_and_captured():
+    """Two layers (one whose sort takes three launches) with their gradients, interleaved on two
+    streams, then both in graphs replayed side by side: the bits of each alone."""
+    layers = [Layer(300, 8, 8, 256, 256, 5), Layer(9, 64, 8, 256, 128, 6)]
+    outs = []
+    for a in layers:
+        a.d_y, a.d_w = torch.zeros_like(a.y), torch.zeros_like(a.w)
+        a.d_x, a.d_logits = torch.zeros_like(a.out), torch.zeros_like(a.logits)
+
+    def step(a):
+        a.run()
+        binding.combine_rows_backward(a.x, a.y, a.rows, a.w, a.d_y, a.d_w)
+        binding.combine_rows(a.d_y, a.rows, a.d_x, resid=a.x)
+        binding.route_backward(None, a.ids, a.w, a.d_w, a.d_logits)
+
+    def results(a):
+        return [a.ids, a.rows, a.offsets, a.out, a.d_y, a.d_w, a.d_x, a.d_logits]
+
+    for a in layers:
+        step(a)
+        torch.cuda.synchronize()
+        outs.append([t.clone() for t in results(a)])
+
+    def check(what):
+        torch.cuda.synchronize()
+        for a, ref in zip(layers, outs):
+            for i, (t, r) in enumerate(zip(results(a), ref)):
+                assert torch.equal(t, r), (what, i)
+                t.zero_()
+        torch.cuda.synchronize()
+
+    check("alone")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for a, s in zip(layers, streams):
+            with torch.cuda.stream(s):
+                step(a)
+        check("streams")
+    graphs = []
+    for a in layers:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(a)
+        graphs.append(g)
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        check("graphs")
+        step(layers[0])                                # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(torch.equal(t, r) for t, r in zip(results(layers[0]), outs[0]))
 
 
 @pytest.mark.parametrize("T,K,E,H", [(20, 3, 8, 40), (300, 4, 8, 64)])
