@@ -36,7 +36,11 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi) {
 
 // One block of 128, 32 codes per lane of each operand, summed from zero by the bf16 matrix
 // instruction: the products are exact in fp32 and so, nearly, is their sum (within 2^-20 of
-// the largest).
+// the largest).  The fp8 instruction, at twice the rate, is no choice: it aligns each eight
+// products (k .. k+7) to the largest of them and drops what lies 13 bits below its leading one
+// (measured), so where large products cancel nothing that is left of the sum need be right.
+// What that costs where the matrix rate binds: 32768 rows of 64 groups, N = K = 4096, take 1150
+// us, 685 with it; 512 rows of 97 groups, 4096 x 1536, where memory binds, 110 against 107.
 struct Wide {
     bf16x8_t v[4];
 };
@@ -159,21 +163,8 @@ __device__ __forceinline__ float silu_mul(float gate, float up) {
 // The waves form WW x WT; each computes 16 FA matrix rows x 16 FB token rows.  The matrix
 // rows of a wave are dealt to its FA fragments four at a time, so that the fragments'
 // accumulators of one lane are consecutive columns of the output.
-//
-// bf16 outputs use the fp8 matrix instruction (twice the bf16 rate).  It aligns each eight
-// products (k .. k+7) to the largest of them and keeps 13 bits below its leading one
-// (measured), so a block's sum is off by less than 2^-10 of the sum over the eights of their
-// largest product; on normal inputs by 2^-16 of the result, with one channel in a hundred
-// sixteen times the others by 2^-11: below the 2^-9 that the rounding to bf16 is off by.
-// fp32 outputs and SwiGLU (whose e4m3 codes would fall to the other side of a border too often:
-// 2.5e-3 against 1.7e-3 off behind the second product) use the bf16 instruction on the widened
-// codes instead.
-typedef __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ f32x4_t mfma_codes(const i32x8_t& a, const i32x8_t& b) {
-    const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
-}
+typedef __attribute__((address_space(3))) char lds_char;
 
 // 16 (or 4) bytes per lane from memory to LDS: lane i's go to lds + 16 i (4 i).  The compiler
 // does not count these loads: the kernel waits for them itself, before its barrier.  M0 holds
@@ -214,7 +205,7 @@ struct Shape {
 
 template <class C, int OUT>
 __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nblocks, int kb_n) {
-    constexpr bool GATED = OUT == OUT_SWIGLU, WIDEN = OUT != OUT_BF16;
+    constexpr bool GATED = OUT == OUT_SWIGLU;
     constexpr int FA = C::FA, FB = C::FB, NA = C::NA, NB = C::NB, TT = C::TT, WAVES = C::WAVES;
     constexpr int HF = GATED ? FA / 2 : FA;               // fragments of one half
     constexpr int CF = HF < 4 ? HF : 4;                   // fragments that share runs of columns
@@ -373,7 +364,7 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nb
         for (int m = 0; m < FB; ++m) xs[m] = sc[(wt * 16 * FB + m * 16 + l16) * each];
         const float w0 = sc[TT * each], w1 = sc[(TT + 1) * each];
         f32x4_t part[P];
-        Wide bw[WIDEN ? FB : 1], aw;
+        Wide bw[FB], aw;
         auto add = [&](int i) {
             const int j = i / FB, m = i % FB;
             const float ws = GATED ? (j < HF ? w0 : w1) : (ww * 16 * FA + j * 16) < kBlock ? w0 : w1;
@@ -387,16 +378,12 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nb
             if (AR > 1 && j + 1 < FA) fragment(av[(j + 1) % AR], st, a0 + (j + 1) * 2048);
             if (j == FA - 1) meet(kb, stage, next);
             if (AR > 1 && j + 1 == FA) fragment(av[(j + 1) % AR], nx, a0);
-            if constexpr (WIDEN) aw = widen_block(av[j % AR]);
+            aw = widen_block(av[j % AR]);
 #pragma unroll
             for (int m = 0; m < FB; ++m) {
                 const int i = j * FB + m;
-                if constexpr (WIDEN) {
-                    if (j == 0) bw[m] = widen_block(b[m]);
-                    part[i % P] = mfma_block(aw, bw[m]);
-                } else {
-                    part[i % P] = mfma_codes(av[j % AR], b[m]);
-                }
+                if (j == 0) bw[m] = widen_block(b[m]);
+                part[i % P] = mfma_block(aw, bw[m]);
                 if (j + 1 == FA) fragment(b[m], nx, b0 + m * 2048);
                 if (i >= P - 1) add(i - (P - 1));
                 __builtin_amdgcn_sched_barrier(0);
@@ -520,11 +507,10 @@ hipError_t product(const ProductArgs& a, hipStream_t s) {
 // (256 CUs).  The largest one wins whose tiles the groups fill and which still gives nearly
 // every CU a workgroup.  Measured (us; both sides of each border; N 4096 and 64 groups where
 // nothing else is said; SwiGLU: both products of an expert, hidden 2048 and inter 1024):
-//   256 x 256 / 256 x 128   32768 rows, K 4096: 660 / 738;  16384 rows, N 2048, K 1024: 84 / 84
-//   256 x 128 / 128 x 64    4096 rows, K 2048: 125 / 129;  one group, 1024 x 1024, K 4096: 36 / 22
-//   128 x 64 / 128 x 16     1024 rows, K 2048: 98 / 105;  32 rows of 25 groups, K 1024: 12.7 / 11.6
-//   128 x 64 / 64 x 32      one group, 333 x 1000, K 1040: 9.9 / 6.8
-//   64 x 32 / 32 x 16       one group, N 2048, K 2048: 128 rows 8.3 / 8.4, 64 rows 8.2 / 7.4
+//   256 x 128 / 128 x 64    32768 rows, K 4096: 1162 / 1462;  4096 rows, K 2048: 164 / 167
+//   128 x 64 / 128 x 16     1024 rows, K 2048: 114 / 110, 512 rows: 104 / 90;  32 rows of 25 groups, K 1024: 17.1 / 13.2
+//   128 x 64 / 64 x 32      one group: 2048 x 2048, K 4096: 50 / 78;  1024 x 1024, K 4096: 32 / 24;  333 x 1000, K 1040: 12.7 / 8.3
+//   64 x 32 / 32 x 16       one group, N 2048, K 2048: 128 rows 11.0 / 10.9, 64 rows 10.5 / 9.2
 //   SwiGLU 256 x 128 / 64   16384 rows: 275 / 316;  2048 rows: 113 / 114;  1024 rows: 100 / 98
 //   SwiGLU 256 x 64 / 32    one group: 2000 rows 38 / 51, 1000 rows 36 / 28
 //   SwiGLU 256 x 32 / 16    512 rows: 78 / 90;  64 rows: 53 / 51
@@ -535,8 +521,6 @@ hipError_t by_size(const ProductArgs& a, hipStream_t s) {
         return (int64_t)((a.N + TW - 1) / TW) * most_tiles(a, TT) >= least;
     };
     constexpr int64_t kMost = 192;
-    if constexpr (OUT == OUT_BF16)   // the widened codes of 256 x 256 do not fit the registers
-        if (avg >= 384 && fills(256, 256, kMost)) return product<Shape<256, 256, 8, 2>, OUT>(a, s);
     if (avg >= 32 && fills(256, 128, kMost)) return product<Shape<256, 128, 8, 3>, OUT>(a, s);
     if constexpr (OUT == OUT_SWIGLU) {
         if (avg >= 16 && fills(256, 64, kMost)) return product<Shape<256, 64, 8, 3>, OUT>(a, s);
