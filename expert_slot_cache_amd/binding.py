@@ -448,6 +448,8 @@ def _rows(name: str, t, dev: int):
 
 
 def _atype(torch, name: str, t) -> int:
+    if t is None:
+        _bad(f"{name} is missing")
     dtype = t.dtype
     if dtype is torch.bfloat16:
         return A_BF16
@@ -513,7 +515,7 @@ def sort_tokens(x, topk_ids, sorted_x, offsets, rows, *, scales=None, workspace=
     dev, s = _place(torch, stream)
     shape = T, K = _array("topk_ids", topk_ids, torch.int32, dev)
     _check_tensor("rows", rows, torch.int32, shape, dev)
-    E = min(offsets.numel() - 1, 0x7fffffff)
+    E = _sizes("offsets", offsets, 1)[0] - 1
     _check_tensor("offsets", offsets, torch.int32, (E + 1,), dev)
     H = at = f8 = stride = 0
     if x is None:
@@ -548,6 +550,7 @@ def combine_rows(ys, rows, out, *, topk_w=None, resid=None, stream=None):
     import torch
     dev, s = _place(torch, stream)
     shape = T, K = _array("rows", rows, torch.int32, dev)
+    at = _atype(torch, "out", out)
     n, H = _array("out", out, out.dtype, dev)
     if n != T:
         _bad(f"out has {n} rows, rows {T}")
@@ -556,7 +559,7 @@ def combine_rows(ys, rows, out, *, topk_w=None, resid=None, stream=None):
         _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
     if resid is not None:
         _check_tensor("resid", resid, out.dtype, (T, H), dev)
-    _check(lib().moe_combine_rows(_atype(torch, "out", out), ys.data_ptr(), rows.data_ptr(), _ptr(topk_w), _ptr(resid),
+    _check(lib().moe_combine_rows(at, ys.data_ptr(), rows.data_ptr(), _ptr(topk_w), _ptr(resid),
                                   T, K, H, out.data_ptr(), s))
 
 
@@ -566,6 +569,7 @@ def combine_rows_backward(d_out, ys, rows, topk_w, d_ys, d_topk_w, *, stream=Non
     import torch
     dev, s = _place(torch, stream)
     shape = T, K = _array("rows", rows, torch.int32, dev)
+    at = _atype(torch, "d_out", d_out)
     n, H = _array("d_out", d_out, d_out.dtype, dev)
     if n != T:
         _bad(f"d_out has {n} rows, rows {T}")
@@ -573,9 +577,8 @@ def combine_rows_backward(d_out, ys, rows, topk_w, d_ys, d_topk_w, *, stream=Non
     _check_tensor("d_ys", d_ys, d_out.dtype, (T * K, H), dev)
     _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
     _check_tensor("d_topk_w", d_topk_w, torch.float32, shape, dev)
-    _check(lib().moe_combine_rows_backward(_atype(torch, "d_out", d_out), d_out.data_ptr(), ys.data_ptr(),
-                                           rows.data_ptr(), topk_w.data_ptr(), T, K, H, d_ys.data_ptr(),
-                                           d_topk_w.data_ptr(), s))
+    _check(lib().moe_combine_rows_backward(at, d_out.data_ptr(), ys.data_ptr(), rows.data_ptr(), topk_w.data_ptr(),
+                                           T, K, H, d_ys.data_ptr(), d_topk_w.data_ptr(), s))
 
 
 def scaled_product(x, x_scales, w, w_scales, out, *, offsets=None, swiglu_scales=None, stream=None):
