@@ -167,16 +167,17 @@ __device__ __forceinline__ float silu_mul(float gate, float up) {
 typedef __attribute__((address_space(3))) char lds_char;
 
 // 16 (or 4) bytes per lane from memory to LDS: lane i's go to lds + 16 i (4 i).  The compiler
-// does not count these loads: the kernel waits for them itself, before its barrier.  M0 holds
-// the LDS address; the compiler keeps nothing there (it sets it right before its own uses).
+// does not count these loads: the kernel waits for them itself, before its barrier.  The LDS
+// address is an operand in M0, which the compiler so knows to be taken; one wait state lies between
+// the two.  A base is a sum made by scalar instructions: a load has to wait for no result of theirs.
 __device__ __forceinline__ void copy16(uint32_t lds, uint32_t voff, const uint8_t* base) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(voff), "s"(base) : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t lds, const float* p) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds), "v"(p) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const float* p) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(lds), "v"(p) : "memory");
 }
 // All but this wave's newest N copies have landed and its LDS reads are done, and so for
 // every wave of the workgroup.
