@@ -15,6 +15,7 @@
 
 #include "ops.hpp"
 #include "ops_dev.hpp"
+#include "product_tile.hpp"
 
 namespace moe {
 namespace {
@@ -186,9 +187,9 @@ __device__ __forceinline__ void wait_and_meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int TW_, int TT_, int WAVES_, int S_>
+template <class T>
 struct Shape {
-    static constexpr int TW = TW_, TT = TT_, WAVES = WAVES_, S = S_;
+    static constexpr int TW = T::TW, TT = T::TT, WAVES = T::WAVES, S = T::S;
     static constexpr int WT = TT > 64 ? TT / 64 : 1;       // waves along tokens,
     static constexpr int WW = WAVES / WT;                  // along matrix rows
     static constexpr int FA = TW / WW / 16, FB = TT / WT / 16;   // fragments of a wave
@@ -486,61 +487,29 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_product(ProductArgs a, int nb
     }
 }
 
-// Tiles of TM rows that the groups can have: each group's last one may be short.
-int64_t most_tiles(const ProductArgs& a, int TM) {
-    const int64_t full = ((int64_t)a.M + TM - 1) / TM;
-    if (!a.offsets) return full;
-    return (int64_t)a.M / TM + (a.G < a.M ? a.G : a.M);
-}
-
 template <class C, int OUT>
 hipError_t product(const ProductArgs& a, hipStream_t s) {
     constexpr int COLS = OUT == OUT_SWIGLU ? C::TW / 2 : C::TW;
     const int cols = OUT == OUT_SWIGLU ? a.N / 2 : a.N;
     const int nblocks = (cols + COLS - 1) / COLS, kb_n = (a.K + kBlock - 1) / kBlock;
-    const int64_t grid = (nblocks * most_tiles(a, C::TT) + 7) / 8 * 8;
+    const int64_t grid = (nblocks * most_tiles(a.M, a.G, a.offsets, C::TT) + 7) / 8 * 8;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_product<C, OUT>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, a, nblocks, kb_n);
     return hipGetLastError();
 }
 
-// The shape, by the rows that a group has on average and by the workgroups that a shape gives
-// (256 CUs).  The largest one wins whose tiles the groups fill and which still gives nearly
-// every CU a workgroup.  Measured (us; both sides of each border; N 4096 and 64 groups where
-// nothing else is said; SwiGLU: both products of an expert, hidden 2048 and inter 1024):
-//   256 x 128 / 128 x 64    32768 rows, K 4096: 1162 / 1462;  4096 rows, K 2048: 164 / 167
-//   128 x 64 / 128 x 16     1024 rows, K 2048: 114 / 110, 512 rows: 104 / 90;  32 rows of 25 groups, K 1024: 17.1 / 13.2
-//   128 x 64 / 64 x 32      one group: 2048 x 2048, K 4096: 50 / 78;  1024 x 1024, K 4096: 32 / 24;  333 x 1000, K 1040: 12.7 / 8.3
-//   64 x 32 / 32 x 16       one group, N 2048, K 2048: 128 rows 11.0 / 10.9, 64 rows 10.5 / 9.2
-//   SwiGLU 256 x 128 / 64   16384 rows: 275 / 316;  2048 rows: 113 / 114;  1024 rows: 100 / 98
-//   SwiGLU 256 x 64 / 32    one group: 2000 rows 38 / 51, 1000 rows 36 / 28
-//   SwiGLU 256 x 32 / 16    512 rows: 78 / 90;  64 rows: 53 / 51
-template <int OUT>
-hipError_t by_size(const ProductArgs& a, hipStream_t s) {
-    const int64_t avg = a.M / a.G;
-    auto fills = [&](int TW, int TT, int64_t least) {
-        return (int64_t)((a.N + TW - 1) / TW) * most_tiles(a, TT) >= least;
-    };
-    constexpr int64_t kMost = 192;
-    if (avg >= 32 && fills(256, 128, kMost)) return product<Shape<256, 128, 8, 3>, OUT>(a, s);
-    if constexpr (OUT == OUT_SWIGLU) {
-        if (avg >= 16 && fills(256, 64, kMost)) return product<Shape<256, 64, 8, 3>, OUT>(a, s);
-        if (avg >= 6 && fills(256, 32, kMost)) return product<Shape<256, 32, 8, 4>, OUT>(a, s);
-        return product<Shape<256, 16, 8, 4>, OUT>(a, s);
-    } else {
-        if (avg >= 16 && fills(128, 64, kMost)) return product<Shape<128, 64, 4, 3>, OUT>(a, s);
-        if (avg < 16 && fills(128, 16, kMost)) return product<Shape<128, 16, 4, 4>, OUT>(a, s);
-        if (fills(64, 32, 128)) return product<Shape<64, 32, 4, 5>, OUT>(a, s);
-        return product<Shape<32, 16, 2, 8>, OUT>(a, s);
-    }
-}
-
 }  // namespace
 
 hipError_t launch_scaled_product(const ProductArgs& a, int out, hipStream_t s) {
-    if (out == OUT_SWIGLU) return by_size<OUT_SWIGLU>(a, s);
-    if (out == OUT_BF16) return by_size<OUT_BF16>(a, s);
-    return by_size<OUT_F32>(a, s);
+    auto run = [&](auto o) {
+        constexpr int OUT = decltype(o)::value;
+        return product_tile<OUT == OUT_SWIGLU>(a.M, a.G, a.N, a.offsets, [&](auto tile) {
+            return product<Shape<decltype(tile)>, OUT>(a, s);
+        });
+    };
+    if (out == OUT_SWIGLU) return run(std::integral_constant<int, OUT_SWIGLU>{});
+    if (out == OUT_BF16) return run(std::integral_constant<int, OUT_BF16>{});
+    return run(std::integral_constant<int, OUT_F32>{});
 }
 
 }  // namespace moe
