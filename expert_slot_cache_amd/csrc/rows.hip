@@ -387,9 +387,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restric
 
 // W waves take a token and up to eight of its pairs (grid.y walks the groups of pairs): d_out[t]
 // is read once for them, each pair's dot product stays in a register per lane and is summed
-// over the lanes, then the waves, at the end, in a fixed order.  One wave a token when there are
-// enough of them; few tokens are split over more (one token, 12 pairs, 8192 values, fp32:
-// 8.5 us, 35 with one wave).
+// over the lanes, then the waves, at the end, in a fixed order.  How many waves: combine_backward.
 template <int AT, bool STREAM, int W>
 __global__ __launch_bounds__(W > kWaves ? 64 * W : kThreads) void k_combine_rows_backward(const void* __restrict__ dout,
         const void* __restrict__ ys, const int32_t* __restrict__ rows, const float* __restrict__ w, int T, int K, int per,
@@ -525,11 +523,15 @@ hipError_t combine_backward(const void* dout, const void* ys, const int32_t* row
                            dim3(W > kWaves ? 64 * W : kThreads), 0, s, dout, ys, rows, w, T, K, per, H, dys, dw);
         return hipGetLastError();
     };
+    // Several waves walk a row where one a token would leave CUs without one, or where the row fills
+    // most of the steps that four waves take together.  bf16, 8 pairs a token, us with 1 / 4 / 16:
+    // 250 x 4096 43 / 17 / 13, 500 x 4096 45 / 20 / 22; 1000 x 1024 17.2 / 13.0, 1500 x 1024 19.6 /
+    // 21.8; 6000 x 2048 (a whole step) 110 / 90, 6000 x 2560 (1.25 of two) 124 / 128, 6000 x 3000
+    // (1.46 of two) 160 / 139.
     const int64_t waves = (int64_t)T * groups;
-    if constexpr (!STREAM) {                            // few tokens' rows are no large call
-        if (waves < 256 && H > 64 * 4 * Piece<AT>::N) return run(std::integral_constant<int, 16>{});
-        if (waves < 2048 && H > 64 * Piece<AT>::N) return run(std::integral_constant<int, 4>{});
-    }
+    const int pieces = (H + Piece<AT>::N - 1) / Piece<AT>::N, steps = (pieces + 255) / 256;
+    if (waves < 256 && pieces > 256) return run(std::integral_constant<int, 16>{});
+    if (pieces > 64 && (waves < 1280 || 3 * pieces >= 2 * 256 * steps)) return run(std::integral_constant<int, 4>{});
     return run(std::integral_constant<int, 1>{});
 }
 
