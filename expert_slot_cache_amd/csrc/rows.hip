@@ -40,11 +40,19 @@ __host__ __device__ inline int64_t sort_chunk(int64_t P) {
 // Dynamic LDS: base[E] int32, then cnt[kWaves][E] uint16.
 size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2; }
 
-// Rows that are read once are loaded past the caches' retention, and a call whose pairs' rows
-// are more than the L2s hold (kStream bytes) also stores that way: nobody finds them there
-// again (sorting 4096 x 8 rows of 4096 to e4m3 35.7 us, 44.7 with plain stores; combining
-// 4001 x 8 rows of 2048, bf16, 40.2 us against 44.2).  A small call's rows stay for the next kernel.
-constexpr int64_t kStream = (int64_t)32 << 20;
+// Rows that are read once are loaded past the caches' retention.  Whether they are also stored that
+// way goes by the call and the kernel that reads them next, timed together (us, cached / past):
+//  sorted copies, then their combine, 8 a token: of 2048 bf16, 64 MiB 39 / 45, 109 MiB 63 / 67, 128
+//    MiB 82 / 77, 256 MiB 153 / 142: past from 120 MiB on.  (The sort alone: past from 16 MiB on.)
+//  sorted e4m3 rows of 4096, then their product with 512 columns: 4 MiB 40.2 / 39.4, 24 MiB 75.3 /
+//    74.4, 128 MiB 215 / 216; alone 7.5 / 7.3, 16.8 / 14.7, 44 / 36: always past.
+//  the sum of rows of 2048, 8 a token, then an addition to it: rows of 48 MiB 26.5 / 26.4, of 128 MiB
+//    51.2 / 51.7; alone 22.8 / 21.6, 44 / 42: past from rows of 32 MiB on.
+//  its gradient, then the rows' combine: 75 MiB 53.7 / 55.8, 187 MiB 130 / 138, 256 MiB 190.5 / 190,
+//    512 MiB 356 / 344: past what the last cache holds, 256 MiB.
+constexpr int64_t kCopiesPast = (int64_t)120 << 20;
+constexpr int64_t kSumsPast = (int64_t)32 << 20;
+constexpr int64_t kGradientPast = (int64_t)256 << 20;
 
 // Exclusive prefix sums of v[0 .. E) in place, by the whole workgroup; returns the sum.
 __device__ int block_scan(int32_t* v, int E) {
@@ -466,11 +474,10 @@ int lanes_for(int n, int lo) {
     return bx;
 }
 
-template <int AT, bool F8>
+template <int AT, bool F8, bool STREAM>
 hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, int32_t* rows, int32_t* counts,
                 hipStream_t s) {
     Spread a = a0;
-    constexpr int es = AT == A_F32 ? 4 : 2;
     const int pieces = F8 ? a.H / 16 : (a.H + Piece<AT>::N - 1) / Piece<AT>::N;
     a.bx = lanes_for(pieces, 8);
     const int64_t P = (int64_t)a.T * a.K;
@@ -479,14 +486,10 @@ hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, i
     const int tokens_grid = (a.T + by - 1) / by;
     // few tokens: a row's pieces go over several workgroups
     const int columns = tokens_grid < 512 ? (pieces + a.bx - 1) / a.bx : 1;
-    const bool stream = P * a.H * (F8 ? 1 : es) > kStream;
     if (P <= kOneLaunch) {
         const int across = std::min(columns, std::max(kSorters / std::max(tokens_grid, 1), 1));
         const dim3 grid = a.x ? dim3(std::min(tokens_grid, kSorters), across) : dim3(1);
-        if (stream)
-            hipLaunchKernelGGL((k_sort_one<AT, F8, true>), grid, dim3(kThreads), sort_lds(E), s, a, ids, E, bits, offsets, rows);
-        else
-            hipLaunchKernelGGL((k_sort_one<AT, F8, false>), grid, dim3(kThreads), sort_lds(E), s, a, ids, E, bits, offsets, rows);
+        hipLaunchKernelGGL((k_sort_one<AT, F8, STREAM>), grid, dim3(kThreads), sort_lds(E), s, a, ids, E, bits, offsets, rows);
         return hipGetLastError();
     }
     const dim3 grid(tokens_grid, columns);
@@ -496,10 +499,7 @@ hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, i
     hipLaunchKernelGGL(k_sort_place, dim3(nb), dim3(kThreads), sort_lds(E), s, ids, P, chunk, E, bits, counts, offsets,
                        rows);
     if (!a.x) return hipGetLastError();
-    if (stream)
-        hipLaunchKernelGGL((k_spread<AT, F8, true>), grid, dim3(kThreads), 0, s, a, rows);
-    else
-        hipLaunchKernelGGL((k_spread<AT, F8, false>), grid, dim3(kThreads), 0, s, a, rows);
+    hipLaunchKernelGGL((k_spread<AT, F8, STREAM>), grid, dim3(kThreads), 0, s, a, rows);
     return hipGetLastError();
 }
 
@@ -549,14 +549,19 @@ hipError_t launch_sort(int atype, const void* x, int64_t stride, const int32_t* 
                        hipStream_t s) {
     const Spread a{x, stride, T, K, H, 0, sorted, scales};
     int32_t* counts = static_cast<int32_t*>(workspace);
-    if (atype == A_F32)
-        return f8 ? sort<A_F32, true>(a, ids, E, offsets, rows, counts, s) : sort<A_F32, false>(a, ids, E, offsets, rows, counts, s);
-    return f8 ? sort<A_BF16, true>(a, ids, E, offsets, rows, counts, s) : sort<A_BF16, false>(a, ids, E, offsets, rows, counts, s);
+    auto run = [&](auto at) {
+        constexpr int AT = decltype(at)::value;
+        if (f8) return sort<AT, true, true>(a, ids, E, offsets, rows, counts, s);
+        const bool stream = (int64_t)T * K * H * (AT == A_F32 ? 4 : 2) > kCopiesPast;
+        return stream ? sort<AT, false, true>(a, ids, E, offsets, rows, counts, s)
+                      : sort<AT, false, false>(a, ids, E, offsets, rows, counts, s);
+    };
+    return atype == A_F32 ? run(std::integral_constant<int, A_F32>{}) : run(std::integral_constant<int, A_BF16>{});
 }
 
 hipError_t launch_combine(int atype, const void* ys, const int32_t* rows, const float* w, const void* resid, int T,
                           int K, int H, void* out, hipStream_t s) {
-    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kStream;
+    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kSumsPast;
     if (atype == A_F32)
         return stream ? combine<A_F32, true>(ys, rows, w, resid, T, K, H, out, s)
                       : combine<A_F32, false>(ys, rows, w, resid, T, K, H, out, s);
@@ -566,7 +571,7 @@ hipError_t launch_combine(int atype, const void* ys, const int32_t* rows, const 
 
 hipError_t launch_combine_backward(int atype, const void* dout, const void* ys, const int32_t* rows, const float* w,
                                    int T, int K, int H, void* dys, float* dw, hipStream_t s) {
-    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kStream;
+    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kGradientPast;
     if (atype == A_F32)
         return stream ? combine_backward<A_F32, true>(dout, ys, rows, w, T, K, H, dys, dw, s)
                       : combine_backward<A_F32, false>(dout, ys, rows, w, T, K, H, dys, dw, s);
