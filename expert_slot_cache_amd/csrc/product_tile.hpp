@@ -22,12 +22,14 @@ inline int64_t most_tiles(int64_t M, int64_t G, bool offsets, int TM) {
 // every CU a workgroup.  Measured (us; both sides of each border; N 4096 and 64 groups where
 // nothing else is said; SwiGLU: both products of an expert, hidden 2048 and inter 1024):
 //   256 x 128 / 128 x 64    32768 rows, K 4096: 1162 / 1462;  4096 rows, K 2048: 164 / 167
-//   128 x 64 / 128 x 16     1024 rows, K 2048: 114 / 110, 512 rows: 104 / 90;  32 rows of 25 groups, K 1024: 17.1 / 13.2
-//   128 x 64 / 64 x 32      one group: 2048 x 2048, K 4096: 50 / 78;  1024 x 1024, K 4096: 32 / 24;  333 x 1000, K 1040: 12.7 / 8.3
+//   128 x 64 / 128 x 16     1024 rows, K 2048: 114 / 110, 512 rows: 104 / 90;
+//                           32 rows of 25 groups, K 1024: 17.1 / 13.2
+//   128 x 64 / 64 x 32      one group: 2048 x 2048, K 4096: 50 / 78;  1024 x 1024, K 4096: 32 / 24;
+//                           333 x 1000, K 1040: 12.7 / 8.3
 //   64 x 32 / 32 x 16       one group, N 2048, K 2048: 128 rows 11.0 / 10.9, 64 rows 10.5 / 9.2
-//   SwiGLU 256 x 128 / 64   16384 rows: 275 / 316;  2048 rows: 113 / 114;  1024 rows: 100 / 98
-//   SwiGLU 256 x 64 / 32    one group: 2000 rows 38 / 51, 1000 rows 36 / 28
-//   SwiGLU 256 x 32 / 16    512 rows: 78 / 90;  64 rows: 53 / 51
+//   SwiGLU 256 x 128 / 64   16384 rows: 305 / 337;  4096 rows: 145 / 154;  2048 rows: 118 / 122
+//   SwiGLU 256 x 64 / 32    1024 rows: 96 / 98;  one group: 2000 rows 43 / 51, 1000 rows 36 / 30
+//   SwiGLU 256 x 32 / 16    512 rows: 79 / 85;  256 rows: 72 / 70;  64 rows: 54 / 51
 template <bool SWIGLU, class F>
 auto product_tile(int64_t M, int64_t G, int64_t N, bool offsets, F f) {
     const int64_t avg = M / G;

@@ -36,8 +36,8 @@ __device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi) {
 }
 
 // One block of 128, 32 codes per lane of each operand, summed from zero by the bf16 matrix
-// instruction: the products are exact in fp32 and so, nearly, is their sum (within 2^-20 of
-// the largest).  The fp8 instruction, at twice the rate, is no choice: it aligns each eight
+// instruction: the products are exact and added in fp32 (measured off by at most 2^-21 of the sum
+// of their magnitudes; 128 additions of two half steps would be 2^-16).  The fp8 instruction, at twice the rate, is no choice: it aligns each eight
 // products (k .. k+7) to the largest of them and drops what lies 13 bits below its leading one
 // (measured), so where large products cancel nothing that is left of the sum need be right.
 // What that costs where the matrix rate binds: 32768 rows of 64 groups, N = K = 4096, take 1150
@@ -146,8 +146,10 @@ struct Works {
 };
 
 // silu(gate) * up with the hardware's exponential and reciprocal (1 ulp each): within about
-// (4 + |gate|) 2^-24 of the value, far below the half step 2^-4 of the e4m3 code it becomes; the
-// exact quotient and exponential took as long as three stages of a tile.
+// (4 + |gate|) 2^-24 of the value, far below the half step 2^-4 of the e4m3 code it becomes, while
+// the exponential and the reciprocal are normal numbers; from gate = -87.3 on the latter is 0, as
+// the quotient in fp32 is from -88.7 on, and so is the result.  The exact quotient and exponential
+// took as long as three stages of a tile.
 __device__ __forceinline__ float silu_mul(float gate, float up) {
     return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;
 }

@@ -533,8 +533,8 @@ moe_status_t moe_combine_rows_backward(int32_t atype, const void* d_out_dev, con
  * and each 128 x 128 values of a matrix; group g has the rows offsets[g] .. offsets[g+1]:
  *   out[r][n] = sum_b xs[r][b] ws[g][n/128][b] sum_{k in block b} x[r][k] w[g][n][k]
  * The blocks are added in fp32, each times its two scales' product, which has to lie in
- * fp32's range.  A block's products are exact and their sum is held in fp32 (within 2^-20 of
- * the largest of them), for every epilogue: BF16 is F32's output rounded.
+ * fp32's range.  A block's products are exact and added in fp32 (off by less than 2^-16 of the
+ * sum of their magnitudes), for every epilogue: BF16 is F32's output rounded.
  *  x_dev         e4m3 [n_rows][depth], x_scales_dev float [n_rows][ceil(depth/128)].
  *  w_dev         e4m3 [n_groups][n_cols][depth], w_scales_dev float
  *                [n_groups][ceil(n_cols/128)][ceil(depth/128)].  depth: a multiple of 16; x_dev
