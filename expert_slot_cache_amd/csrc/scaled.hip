@@ -147,8 +147,8 @@ struct Works {
 
 // silu(gate) * up with the hardware's exponential and reciprocal (1 ulp each): within about
 // (4 + |gate|) 2^-24 of the value, far below the half step 2^-4 of the e4m3 code it becomes, while
-// the exponential and the reciprocal are normal numbers; from gate = -87.3 on the latter is 0, as
-// the quotient in fp32 is from -88.7 on, and so is the result.  The exact quotient and exponential
+// the exponential and the reciprocal are normal numbers; below gate = -87.3 the latter is none, and
+// below -88.7 the result is 0, as the quotient in fp32 is.  The exact quotient and exponential
 // took as long as three stages of a tile.
 __device__ __forceinline__ float silu_mul(float gate, float up) {
     return gate * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(gate * -1.44269504f)) * up;
