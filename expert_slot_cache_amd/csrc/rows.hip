@@ -526,15 +526,17 @@ hipError_t combine_backward(const void* dout, const void* ys, const int32_t* row
                            dim3(W > kWaves ? 64 * W : kThreads), 0, s, dout, ys, rows, w, T, K, per, H, dys, dw);
         return hipGetLastError();
     };
-    // Several waves walk a row where one a token would leave CUs without one, or where the row fills
-    // most of the steps that four waves take together.  bf16, 8 pairs a token, us with 1 / 4 / 16:
-    // 250 x 4096 43 / 17 / 13, 500 x 4096 45 / 20 / 22; 1000 x 1024 17.2 / 13.0, 1500 x 1024 19.6 /
-    // 21.8; 6000 x 2048 (a whole step) 110 / 90, 6000 x 2560 (1.25 of two) 124 / 128, 6000 x 3000
-    // (1.46 of two) 160 / 139.
+    // Several waves walk a row where one a token would leave CUs without one, or where a token's rows
+    // are long in all and fill most of the steps that four waves take together.  bf16, us with 1 / 4
+    // / 16: 250 x 8 x 4096 43 / 17 / 13, 500 x 8 x 4096 45 / 20 / 22; 1000 x 8 x 1024 17.2 / 13.0,
+    // 1500 x 8 x 1024 19.6 / 21.8; 6000 x 8 x 2048 (a whole step) 110 / 90, 6000 x 8 x 2560 (1.25 of
+    // two) 124 / 128, 6000 x 8 x 3000 (1.46 of two) 160 / 139; 10000 x 1 x 4096 (512 pieces) 53.7 / 57.3,
+    // 10000 x 4 x 2048 (1024) 82.3 / 81.3, 10000 x 4 x 4096 (2048) 166 / 140.
     const int64_t waves = (int64_t)T * groups;
     const int pieces = (H + Piece<AT>::N - 1) / Piece<AT>::N, steps = (pieces + 255) / 256;
     if (waves < 256 && pieces > 256) return run(std::integral_constant<int, 16>{});
-    if (pieces > 64 && (waves < 1280 || 3 * pieces >= 2 * 256 * steps)) return run(std::integral_constant<int, 4>{});
+    if (pieces > 64 && (waves < 1280 || (3 * pieces >= 2 * 256 * steps && per * pieces > 1024)))
+        return run(std::integral_constant<int, 4>{});
     return run(std::integral_constant<int, 1>{});
 }
 
