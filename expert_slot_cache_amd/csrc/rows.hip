@@ -42,16 +42,17 @@ size_t sort_lds(int E) { return (size_t)E * 4 + (size_t)kWaves * E * 2; }
 
 // Rows that are read once are loaded past the caches' retention.  Whether they are also stored that
 // way goes by the call and the kernel that reads them next, timed together (us, cached / past):
-//  sorted copies, then their combine, 8 a token: of 2048 bf16, 64 MiB 39 / 45, 109 MiB 63 / 67, 128
-//    MiB 82 / 77, 256 MiB 153 / 142: past from 120 MiB on.  (The sort alone: past from 16 MiB on.)
-//  sorted e4m3 rows of 4096, then their product with 512 columns: 4 MiB 40.2 / 39.4, 24 MiB 75.3 /
-//    74.4, 128 MiB 215 / 216; alone 7.5 / 7.3, 16.8 / 14.7, 44 / 36: always past.
-//  the sum of rows of 2048, 8 a token, then an addition to it: rows of 48 MiB 26.5 / 26.4, of 128 MiB
-//    51.2 / 51.7; alone 22.8 / 21.6, 44 / 42: past from rows of 32 MiB on.
-//  its gradient, then the rows' combine: 75 MiB 53.7 / 55.8, 187 MiB 130 / 138, 256 MiB 190.5 / 190,
-//    512 MiB 356 / 344: past what the last cache holds, 256 MiB.
+//  sorted copies, then their combine, of 2048 bf16: 8 a token 64 MiB 39 / 45, 109 MiB 63 / 67, 128 MiB
+//    82 / 77, 256 MiB 153 / 142; 1 a token 96 MiB 104 / 107, 128 MiB 144 / 136: past from 120 MiB on.
+//    (The sort alone: past from 16 MiB on.)
+//  sorted e4m3 rows of 4096, then their product with 512 columns: 8 a token 4 MiB 40.2 / 39.4, 24 MiB
+//    75.3 / 74.4, 128 MiB 215 / 216; 1 a token 16 MiB 63.0 / 64.2; alone 8 a token 16.8 / 14.7 at 24
+//    MiB, 44 / 36 at 128: always past.
+//  the sum of rows of 2048, then an addition to it: 8 a token, rows of 128 MiB 51.2 / 51.7; 2 a token,
+//    of 64 MiB 44 / 46; 1 a token 68 / 72; alone 44.3 / 42.3, 32.6 / 31.8, 47.5 / 45.9: never past.
+//  its gradient, then the rows' combine: 8 a token 75 MiB 53.7 / 55.8, 187 MiB 130 / 138, 256 MiB
+//    190.5 / 190, 512 MiB 356 / 344: past what the last cache holds, 256 MiB.
 constexpr int64_t kCopiesPast = (int64_t)120 << 20;
-constexpr int64_t kSumsPast = (int64_t)32 << 20;
 constexpr int64_t kGradientPast = (int64_t)256 << 20;
 
 // Exclusive prefix sums of v[0 .. E) in place, by the whole workgroup; returns the sum.
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(kThreads) void k_spread(Spread a, const int32_t* __
 }
 
 // ---- back: the weighted sum -------------------------------------------------------------
-template <int AT, bool STREAM>
+template <int AT>
 __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restrict__ ys, const int32_t* __restrict__ rows,
         const float* __restrict__ w, const void* __restrict__ resid, int T, int K, int H, int bx,
         void* __restrict__ out) {
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_rows(const void* __restric
 #pragma unroll
             for (int i = 0; i < V::N; ++i) acc.v[i] += r.v[i];
         }
-        acc.template store<FULL, STREAM>(out, (int64_t)t * H + c, left);
+        acc.template store<FULL, false>(out, (int64_t)t * H + c, left);
     };
     if (c + V::N <= H) piece(std::true_type{});
     else piece(std::false_type{});
@@ -506,12 +507,12 @@ hipError_t sort(const Spread& a0, const int32_t* ids, int E, int32_t* offsets, i
     return hipGetLastError();
 }
 
-template <int AT, bool STREAM>
+template <int AT>
 hipError_t combine(const void* ys, const int32_t* rows, const float* w, const void* resid, int T, int K, int H,
                    void* out, hipStream_t s) {
     const int n = (H + Piece<AT>::N - 1) / Piece<AT>::N;
     const int bx = lanes_for(n, 8), by = kThreads / bx;
-    hipLaunchKernelGGL((k_combine_rows<AT, STREAM>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0, s, ys,
+    hipLaunchKernelGGL((k_combine_rows<AT>), dim3((T + by - 1) / by, (n + bx - 1) / bx), dim3(kThreads), 0, s, ys,
                        rows, w, resid, T, K, H, bx, out);
     return hipGetLastError();
 }
@@ -566,12 +567,8 @@ hipError_t launch_sort(int atype, const void* x, int64_t stride, const int32_t* 
 
 hipError_t launch_combine(int atype, const void* ys, const int32_t* rows, const float* w, const void* resid, int T,
                           int K, int H, void* out, hipStream_t s) {
-    const bool stream = (int64_t)T * K * H * (atype == A_F32 ? 4 : 2) > kSumsPast;
-    if (atype == A_F32)
-        return stream ? combine<A_F32, true>(ys, rows, w, resid, T, K, H, out, s)
-                      : combine<A_F32, false>(ys, rows, w, resid, T, K, H, out, s);
-    return stream ? combine<A_BF16, true>(ys, rows, w, resid, T, K, H, out, s)
-                  : combine<A_BF16, false>(ys, rows, w, resid, T, K, H, out, s);
+    if (atype == A_F32) return combine<A_F32>(ys, rows, w, resid, T, K, H, out, s);
+    return combine<A_BF16>(ys, rows, w, resid, T, K, H, out, s);
 }
 
 hipError_t launch_combine_backward(int atype, const void* dout, const void* ys, const int32_t* rows, const float* w,

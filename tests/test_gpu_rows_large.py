@@ -26,7 +26,7 @@ def tokens(T, H, seed, kind):
     return torch.randn(T, H, generator=gen, device=DEV).to(ops.TYPES[kind])
 
 
-# (tokens, k, hidden, type): rows of 32, 120 and 256 MiB lie between these
+# (tokens, k, hidden, type): rows of 120 and 256 MiB lie between these
 LARGE = [(1000, 8, 2048, "bf16"), (1030, 8, 2050, "bf16"), (3700, 8, 2048, "bf16"), (3901, 8, 2056, "bf16"), (3100, 5, 2049, "f32"),
          (4000, 8, 4096, "bf16"), (4200, 8, 4100, "bf16"), (260, 33, 8192, "f32")]
 
