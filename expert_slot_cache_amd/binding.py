@@ -33,6 +33,8 @@ EVICT_LRU, EVICT_FIFO, EVICT_LFU, EVICT_SLRU, EVICT_DECAY = 0, 1, 2, 3, 4
 EVICTS = {"lru": EVICT_LRU, "fifo": EVICT_FIFO, "lfu": EVICT_LFU, "slru": EVICT_SLRU, "decay": EVICT_DECAY}
 ROUTE_SOFTMAX, ROUTE_RENORM = 0, 1
 PRODUCT_F32, PRODUCT_BF16, PRODUCT_SWIGLU = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
 PREFETCH_AFTER = {"layer": 0, "queued": 1, "previous": 2}
 
 
@@ -117,6 +119,13 @@ _SIGS = {
     "moe_combine_rows": (_I32, [_I32, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P]),
     "moe_combine_rows_backward": (_I32, [_I32, _P, _P, _P, _P, _I32, _I32, _I32, _P, _P, _P]),
     "moe_scaled_product": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_route_groups": (_I32, [_I32, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I32, C.c_float, _P, _P, _P]),
+    "moe_route_groups_backward": (_I32, [_I32, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, C.c_float, _P, _I64, _P]),
+    "moe_expert_product": (_I32, [_I32, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
+    "moe_activation_backward": (_I32, [_I32, _P, _I32, _P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, C.c_size_t, _P]),
+    "moe_activation_backward_workspace_bytes": (C.c_size_t, [_I32, _I32, _I32]),
+    "moe_expert_product_backward": (_I32, [_I32, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P, _I32, _P, _P, C.c_size_t, _P]),
+    "moe_expert_product_backward_workspace_bytes": (C.c_size_t, [_I32, _I32, _I32, _I32, _I32]),
     "moe_lru_create": (_I32, [_I32, _I32, _I32, C.POINTER(_P)]),
     "moe_lru_destroy": (None, [_P]),
     "moe_lru_step": (_I32, [_P, _P, _I32, _I32, _P, C.POINTER(Miss), _I32, _PI32, _PI32]),
@@ -499,6 +508,57 @@ def route_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, *, renorm: bool
                                     ROUTE_RENORM if renorm else ROUTE_SOFTMAX, d_logits.data_ptr(), d_stride, s))
 
 
+def _named(what: str, names: dict, name) -> int:
+    if name not in names:
+        _bad(f"{what} {name!r}: one of {', '.join(names)}")
+    return names[name]
+
+
+def route_groups(logits, topk_ids, topk_w, *, bias=None, score: str = "softmax", renorm: bool = True, n_groups: int = 1,
+                 kept_groups: int | None = None, group_top: int = 1, scale: float = 1.0, stream=None):
+    """moe_route_groups: logits [T, E] (fp32 or bf16, rows may be apart) -> topk_ids int32 [T, K] and
+    topk_w fp32 [T, K], chosen by score ("softmax" or "sigmoid") plus bias fp32 [E] among the
+    kept_groups (None: all) of n_groups groups whose group_top largest choices sum highest."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, E, stride = _rows("logits", logits, dev)
+    shape = _array("topk_ids", topk_ids, torch.int32, dev)
+    if shape[0] != T:
+        _bad(f"topk_ids has {shape[0]} rows, logits {T}")
+    _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
+    if bias is not None:
+        _check_tensor("bias", bias, torch.float32, (E,), dev)
+    at, code = _atype(torch, "logits", logits), _named("score", SCORES, score)
+    _check(lib().moe_route_groups(at, logits.data_ptr(), stride, _ptr(bias), T, E, shape[1], code,
+                                  ROUTE_RENORM if renorm else ROUTE_SOFTMAX, n_groups,
+                                  n_groups if kept_groups is None else kept_groups, group_top, scale, topk_ids.data_ptr(),
+                                  topk_w.data_ptr(), s))
+
+
+def route_groups_backward(logits, topk_ids, topk_w, d_topk_w, d_logits, *, score: str = "softmax", renorm: bool = True,
+                          scale: float = 1.0, stream=None):
+    """moe_route_groups_backward: d_topk_w fp32 [T, K] -> d_logits [T, E] in the logits' type, for
+    what route_groups gave on these logits with this score, renorm and scale (softmax with renorm
+    does not read them: they may be None)."""
+    import torch
+    dev, s = _place(torch, stream)
+    T, E, d_stride = _rows("d_logits", d_logits, dev)
+    stride = E
+    if logits is not None:
+        n, e, stride = _rows("logits", logits, dev)
+        if (n, e) != (T, E) or logits.dtype is not d_logits.dtype:
+            _bad(f"logits are {logits.dtype} {(n, e)}, d_logits {d_logits.dtype} {(T, E)}")
+    shape = _array("topk_ids", topk_ids, torch.int32, dev)
+    if shape[0] != T:
+        _bad(f"topk_ids has {shape[0]} rows, d_logits {T}")
+    _check_tensor("topk_w", topk_w, torch.float32, shape, dev)
+    _check_tensor("d_topk_w", d_topk_w, torch.float32, shape, dev)
+    at, code = _atype(torch, "d_logits", d_logits), _named("score", SCORES, score)
+    _check(lib().moe_route_groups_backward(at, _ptr(logits), stride, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                           d_topk_w.data_ptr(), T, E, shape[1], code, ROUTE_RENORM if renorm else ROUTE_SOFTMAX,
+                                           scale, d_logits.data_ptr(), d_stride, s))
+
+
 def sort_workspace_bytes(n_tokens: int, top_k: int, experts: int) -> int:
     if max(n_tokens, top_k, experts) > 0x7fffffff:
         return 0
@@ -607,6 +667,136 @@ def scaled_product(x, x_scales, w, w_scales, out, *, offsets=None, swiglu_scales
         _check_tensor("out", out, out.dtype, (M, N), dev)
     _check(lib().moe_scaled_product(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), _ptr(offsets),
                                     M, G, N, K, ep, out.data_ptr(), _ptr(swiglu_scales), s))
+
+
+def _workspace(torch, what: str, workspace, need: int, dev: int, like, stream):
+    """The caller's workspace, or one of torch's allocator for this call; and its bytes."""
+    if workspace is not None:
+        _check_tensor("workspace", workspace, torch.uint8, workspace.shape, dev)
+        return workspace, workspace.numel()
+    if need == 0:
+        return None, 0
+    if stream is not None and stream != torch.cuda.current_stream(dev).cuda_stream:
+        _bad(f"{what} on a stream that is not torch's current one needs its workspace from the caller")
+    return torch.empty(need, dtype=torch.uint8, device=like.device), need
+
+
+def _same_or_f32(torch, name: str, t, kind) -> int:
+    at = _atype(torch, name, t)
+    if t.dtype is not kind and at != A_F32:
+        _bad(f"{name} is {t.dtype}, not float32 or {kind}")
+    return at
+
+
+def expert_product(x, w, out, *, bias=None, resid=None, pre=None, act: str = "none", offsets=None, stream=None):
+    """moe_expert_product: rows x [M, K] (fp32 or bf16), sorted by group as offsets int32 [G + 1] says
+    (None: one group), times w [G, N, K] of their type; with bias fp32 [G, N], act ("none", "relu",
+    "gelu", "silu" or "swiglu") and resid into out [M, N] ("swiglu": [M, N/2]), fp32 or x's type.
+    pre [M, N] in x's type gets the values before the activation."""
+    import torch
+    dev, s = _place(torch, stream)
+    at = _atype(torch, "x", x)
+    M, K = _array("x", x, x.dtype, dev)
+    G, N, depth = _array("w", w, x.dtype, dev, 3)
+    if depth != K:
+        _bad(f"rows of w have {depth} values, of x {K}")
+    code = _named("act", ACTS, act)
+    ot = _same_or_f32(torch, "out", out, x.dtype)
+    cols = N // 2 if act == "swiglu" else N
+    _check_tensor("out", out, out.dtype, (M, cols), dev)
+    if bias is not None:
+        _check_tensor("bias", bias, torch.float32, (G, N), dev)
+    if resid is not None:
+        _check_tensor("resid", resid, out.dtype, (M, cols), dev)
+    if pre is not None:
+        _check_tensor("pre", pre, x.dtype, (M, N), dev)
+    if offsets is not None:
+        _check_tensor("offsets", offsets, torch.int32, (G + 1,), dev)
+    _check(lib().moe_expert_product(at, x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(offsets), _ptr(resid), M, G, N, K, code,
+                                    ot, out.data_ptr(), _ptr(pre), s))
+
+
+def activation_backward(d_out, pre, d_pre=None, *, d_bias=None, act: str = "none", offsets=None, workspace=None, stream=None):
+    """moe_activation_backward: d_out [M, N] ("swiglu": [M, N/2]), fp32 or pre's type, and pre [M, N]
+    ("none": not read, may be None) -> d_pre [M, N] in pre's type and d_bias fp32 [G, N] (each
+    optional), for what expert_product took.  workspace: uint8, moe_activation_backward_
+    workspace_bytes(M, G, N) of them where d_bias is given; None: taken from torch's allocator
+    for this call (on torch's current stream only)."""
+    import torch
+    dev, s = _place(torch, stream)
+    code = _named("act", ACTS, act)
+    ot = _atype(torch, "d_out", d_out)
+    M, cols = _array("d_out", d_out, d_out.dtype, dev)
+    N = 2 * cols if act == "swiglu" else cols
+    kind = pre.dtype if pre is not None else d_pre.dtype if d_pre is not None else d_out.dtype
+    if act != "none" or pre is not None:
+        _check_tensor("pre", pre, kind, (M, N), dev)
+    at = A_BF16 if kind is torch.bfloat16 else A_F32
+    _same_or_f32(torch, "d_out", d_out, kind)
+    if d_pre is not None:
+        _atype(torch, "d_pre", d_pre)
+        _check_tensor("d_pre", d_pre, kind, (M, N), dev)
+    G = 1
+    if offsets is not None:
+        G = _sizes("offsets", offsets, 1)[0] - 1
+        _check_tensor("offsets", offsets, torch.int32, (G + 1,), dev)
+    need = 0
+    if d_bias is not None:
+        _check_tensor("d_bias", d_bias, torch.float32, (G, N), dev)
+        need = lib().moe_activation_backward_workspace_bytes(M, G, N) if N <= 0x7fffffff else 0
+    workspace, size = _workspace(torch, "a bias' gradient", workspace, need, dev, d_out, stream)
+    _check(lib().moe_activation_backward(at, d_out.data_ptr(), ot, _ptr(pre), _ptr(offsets), M, G, N, code, _ptr(d_pre),
+                                         _ptr(d_bias), _ptr(workspace), size, s))
+
+
+def activation_backward_workspace_bytes(n_rows: int, n_groups: int, n_cols: int) -> int:
+    if max(n_rows, n_groups, n_cols) > 0x7fffffff:
+        return 0
+    return int(lib().moe_activation_backward_workspace_bytes(n_rows, n_groups, n_cols))
+
+
+def expert_product_backward(d_pre, x, w, *, d_x=None, d_w=None, offsets=None, workspace=None, stream=None):
+    """moe_expert_product_backward: d_pre [M, N] (fp32 or bf16), x [M, K] and w [G, N, K] of its type ->
+    d_x [M, K] in their type and d_w [G, N, K], fp32 or their type (each optional; w is read for
+    d_x alone and x for d_w alone: the other may be None).  workspace: uint8,
+    expert_product_backward_workspace_bytes(...) of them; None: taken from torch's allocator for
+    this call (on torch's current stream only)."""
+    import torch
+    dev, s = _place(torch, stream)
+    at = _atype(torch, "d_pre", d_pre)
+    kind = d_pre.dtype
+    M, N = _array("d_pre", d_pre, kind, dev)
+    if d_x is None and d_w is None:
+        _bad("d_x and d_w are missing")
+    wt, G, K = A_F32, 1, 0
+    if d_w is not None:
+        wt = _same_or_f32(torch, "d_w", d_w, kind)
+        G, n, K = _array("d_w", d_w, d_w.dtype, dev, 3)
+        if n != N:
+            _bad(f"d_w has {n} rows a matrix, d_pre {N} columns")
+        _check_tensor("x", x, kind, (M, K), dev)
+    if d_x is not None:
+        if d_w is None:
+            G, n, K = _array("w", w, kind, dev, 3)
+            if n != N:
+                _bad(f"w has {n} rows a matrix, d_pre {N} columns")
+        else:
+            _check_tensor("w", w, kind, (G, N, K), dev)
+        _check_tensor("d_x", d_x, kind, (M, K), dev)
+    if offsets is not None:
+        _check_tensor("offsets", offsets, torch.int32, (G + 1,), dev)
+    need = lib().moe_expert_product_backward_workspace_bytes(at, M, G, N, K) if d_w is not None else 0
+    workspace, size = _workspace(torch, "a matrix' gradient", workspace, need, dev, d_pre, stream)
+    _check(lib().moe_expert_product_backward(at, d_pre.data_ptr(), x.data_ptr() if d_w is not None else None,
+                                             w.data_ptr() if d_x is not None else None, _ptr(offsets), M, G, N, K, _ptr(d_x),
+                                             wt, _ptr(d_w), _ptr(workspace), size, s))
+
+
+def expert_product_backward_workspace_bytes(kind: str, n_rows: int, n_groups: int, n_cols: int, depth: int) -> int:
+    """kind: "f32" or "bf16", the type of the rows."""
+    if max(n_rows, n_groups, n_cols, depth) > 0x7fffffff:
+        return 0
+    return int(lib().moe_expert_product_backward_workspace_bytes(ATYPES[kind], n_rows, n_groups, n_cols, depth))
 
 
 class SlotLRU:

@@ -1,6 +1,7 @@
 // C entry points of the operators around the experts: argument checks, then one launcher.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 
@@ -65,6 +66,38 @@ moe_status_t check_route(int32_t atype, int64_t stride, int32_t T, int32_t E, in
     return MOE_OK;
 }
 
+moe_status_t check_groups(int32_t atype, int64_t stride, int32_t T, int32_t E, int32_t K, int32_t score, int32_t norm,
+                          float scale, moe::RouteGroups* r) {
+    if (const moe_status_t st = check_route(atype, stride, T, E, K, norm)) return st;
+    CHECK(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, "score %d invalid", score);
+    CHECK(std::isfinite(scale) && scale > 0.0f, "scale %g: finite and above 0", (double)scale);
+    *r = {E, K, 1, 1, 1, score == MOE_SCORE_SIGMOID, norm == MOE_ROUTE_RENORM, scale};
+    return MOE_OK;
+}
+
+// The sizes every product in the activation format shares, a matrix' elements among them.
+moe_status_t check_product(int32_t atype, int32_t M, int32_t G, const int32_t* offsets, int32_t N, int32_t K) {
+    CHECK(atype == MOE_A_F32 || atype == MOE_A_BF16, "atype %d invalid", atype);
+    CHECK(M >= 0 && M <= kMaxPairs, "n_rows %d outside [0,%lld]", M, (long long)kMaxPairs);
+    CHECK(G >= 1 && G <= moe::kMaxExperts, "n_groups %d outside [1,%d]", G, moe::kMaxExperts);
+    CHECK(G == 1 || offsets, "%d groups need offsets", G);
+    CHECK(aligned(offsets, 4), "misaligned offsets");
+    const int32_t each = atype == MOE_A_F32 ? 4 : 8;       // 16 bytes
+    CHECK(N >= each && N <= 2 * kMaxHidden && N % each == 0, "n_cols %d: multiples of %d up to %d", N, each, 2 * kMaxHidden);
+    CHECK(K >= each && K <= kMaxHidden && K % each == 0, "depth %d: multiples of %d up to %d", K, each, kMaxHidden);
+    CHECK((int64_t)M * N <= kMaxElements && (int64_t)M * K <= kMaxElements, "a row array above %lld elements",
+          (long long)kMaxElements);
+    CHECK((int64_t)G * N <= kMaxElements / K, "matrices above %lld elements", (long long)kMaxElements);
+    return MOE_OK;
+}
+
+moe_status_t check_act(int32_t atype, int32_t out_atype, int32_t N, int32_t act) {
+    CHECK(act >= MOE_ACT_NONE && act <= MOE_ACT_SWIGLU, "act %d invalid", act);
+    CHECK(act != MOE_ACT_SWIGLU || N % (atype == MOE_A_F32 ? 8 : 16) == 0, "n_cols %d: SwiGLU needs two halves of 16-byte pieces", N);
+    CHECK(out_atype == MOE_A_F32 || out_atype == atype, "out_atype %d: fp32 or the rows' format", out_atype);
+    return MOE_OK;
+}
+
 moe_status_t check_hidden(int32_t H) {
     CHECK(H >= 1 && H <= kMaxHidden, "hidden %d outside [1,%d]", H, kMaxHidden);
     return MOE_OK;
@@ -103,6 +136,49 @@ moe_status_t moe_route_backward(int32_t atype, const void* logits_dev, int64_t l
                                                n_tokens, n_experts, top_k, norm == MOE_ROUTE_RENORM, d_logits_dev,
                                                d_logits_stride, static_cast<hipStream_t>(stream)),
                     "route_backward");
+}
+
+moe_status_t moe_route_groups(int32_t atype, const void* logits_dev, int64_t logits_stride, const float* bias_dev,
+                              int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t score, int32_t norm,
+                              int32_t n_groups, int32_t kept_groups, int32_t group_top, float scale,
+                              int32_t* topk_ids_dev, float* topk_w_dev, void* stream) {
+    moe::RouteGroups r;
+    if (const moe_status_t st = check_groups(atype, logits_stride, n_tokens, n_experts, top_k, score, norm, scale, &r)) return st;
+    CHECK(n_groups >= 1 && n_groups <= moe::kMaxGroups && n_experts % n_groups == 0,
+          "n_groups %d: divisors of n_experts %d up to %d", n_groups, n_experts, moe::kMaxGroups);
+    CHECK(kept_groups >= 1 && kept_groups <= n_groups, "kept_groups %d outside [1,%d]", kept_groups, n_groups);
+    CHECK(group_top == 1 || group_top == 2, "group_top %d: 1 or 2", group_top);
+    CHECK(top_k <= kept_groups * (n_experts / n_groups), "top_k %d above the %d experts of the kept groups", top_k,
+          kept_groups * (n_experts / n_groups));
+    r.n_groups = n_groups;
+    r.kept = kept_groups;
+    r.group_top = group_top;
+    if (n_tokens == 0) return MOE_OK;
+    CHECK(!bad(logits_dev, act_size(atype)) && aligned(bias_dev, 4) && !bad(topk_ids_dev, 4) && !bad(topk_w_dev, 4),
+          "null or misaligned buffer");
+    return launched(moe::launch_route_groups(atype, logits_dev, logits_stride, bias_dev, n_tokens, r, topk_ids_dev,
+                                             topk_w_dev, static_cast<hipStream_t>(stream)),
+                    "route_groups");
+}
+
+moe_status_t moe_route_groups_backward(int32_t atype, const void* logits_dev, int64_t logits_stride,
+                                       const int32_t* topk_ids_dev, const float* topk_w_dev, const float* d_topk_w_dev,
+                                       int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t score, int32_t norm,
+                                       float scale, void* d_logits_dev, int64_t d_logits_stride, void* stream) {
+    moe::RouteGroups r;
+    if (const moe_status_t st = check_groups(atype, d_logits_stride, n_tokens, n_experts, top_k, score, norm, scale, &r)) return st;
+    const size_t es = act_size(atype);
+    if (r.sigmoid || !r.renorm) {
+        if (const moe_status_t st = check_route(atype, logits_stride, n_tokens, n_experts, top_k, norm)) return st;
+        CHECK(n_tokens == 0 || !bad(logits_dev, es), "null or misaligned buffer");
+    }
+    if (n_tokens == 0) return MOE_OK;
+    CHECK(!bad(topk_ids_dev, 4) && !bad(topk_w_dev, 4) && !bad(d_topk_w_dev, 4) && !bad(d_logits_dev, es),
+          "null or misaligned buffer");
+    return launched(moe::launch_route_groups_backward(atype, logits_dev, logits_stride, topk_ids_dev, topk_w_dev, d_topk_w_dev,
+                                                      n_tokens, r, d_logits_dev, d_logits_stride,
+                                                      static_cast<hipStream_t>(stream)),
+                    "route_groups_backward");
 }
 
 size_t moe_sort_workspace_bytes(int32_t n_tokens, int32_t top_k, int32_t n_experts) {
@@ -201,6 +277,70 @@ moe_status_t moe_scaled_product(const void* x_dev, const float* x_scales_dev, co
     a.N = n_cols;
     a.K = depth;
     return launched(moe::launch_scaled_product(a, epilogue, static_cast<hipStream_t>(stream)), "scaled_product");
+}
+
+moe_status_t moe_expert_product(int32_t atype, const void* x_dev, const void* w_dev, const float* bias_dev,
+                                const int32_t* offsets_dev, const void* resid_dev, int32_t n_rows, int32_t n_groups,
+                                int32_t n_cols, int32_t depth, int32_t act, int32_t out_atype, void* out_dev,
+                                void* pre_dev, void* stream) {
+    if (const moe_status_t st = check_product(atype, n_rows, n_groups, offsets_dev, n_cols, depth)) return st;
+    if (const moe_status_t st = check_act(atype, out_atype, n_cols, act)) return st;
+    if (n_rows == 0) return MOE_OK;
+    CHECK(!bad(x_dev, 16) && !bad(w_dev, 16) && !bad(out_dev, 16) && aligned(resid_dev, 16) && aligned(pre_dev, 16) &&
+              aligned(bias_dev, 4),
+          "null or misaligned buffer (all but the bias and the offsets: 16 bytes)");
+    const moe::ExpertArgs a{x_dev, w_dev, bias_dev, resid_dev, offsets_dev, out_dev, pre_dev, n_rows, n_groups, n_cols, depth, act};
+    return launched(moe::launch_expert_product(atype, out_atype, a, static_cast<hipStream_t>(stream)), "expert_product");
+}
+
+size_t moe_activation_backward_workspace_bytes(int32_t n_rows, int32_t n_groups, int32_t n_cols) {
+    if (n_rows < 0 || n_rows > kMaxPairs || n_groups < 1 || n_groups > moe::kMaxExperts || n_cols < 1 || n_cols > 2 * kMaxHidden)
+        return 0;
+    return moe::activation_workspace(n_rows, n_groups, n_cols);
+}
+
+moe_status_t moe_activation_backward(int32_t atype, const void* d_out_dev, int32_t out_atype, const void* pre_dev,
+                                     const int32_t* offsets_dev, int32_t n_rows, int32_t n_groups, int32_t n_cols,
+                                     int32_t act, void* d_pre_dev, float* d_bias_dev, void* workspace_dev,
+                                     size_t workspace_bytes, void* stream) {
+    const int32_t each = atype == MOE_A_F32 ? 4 : 8;
+    if (const moe_status_t st = check_product(atype, n_rows, n_groups, offsets_dev, n_cols, each)) return st;
+    if (const moe_status_t st = check_act(atype, out_atype, n_cols, act)) return st;
+    CHECK(d_bias_dev || d_pre_dev, "nothing to write");
+    CHECK(aligned(d_bias_dev, 4), "null or misaligned buffer");
+    if (n_rows == 0 && !d_bias_dev) return MOE_OK;
+    CHECK(n_rows == 0 || (!bad(d_out_dev, 16) && (act == MOE_ACT_NONE || !bad(pre_dev, 16)) && aligned(d_pre_dev, 16)),
+          "null or misaligned buffer (all but the bias' gradient and the offsets: 16 bytes)");
+    const size_t need = d_bias_dev ? moe::activation_workspace(n_rows, n_groups, n_cols) : 0;
+    CHECK(need == 0 || (!bad(workspace_dev, 16) && workspace_bytes >= need), "this bias' gradient needs %zu bytes of workspace", need);
+    const moe::ActivationArgs a{d_out_dev, act == MOE_ACT_NONE ? nullptr : pre_dev, offsets_dev, d_pre_dev, d_bias_dev,
+                                static_cast<float*>(workspace_dev), n_rows, n_groups, n_cols, act};
+    return launched(moe::launch_activation_backward(atype, out_atype, a, static_cast<hipStream_t>(stream)), "activation_backward");
+}
+
+size_t moe_expert_product_backward_workspace_bytes(int32_t atype, int32_t n_rows, int32_t n_groups, int32_t n_cols,
+                                                   int32_t depth) {
+    const int32_t any = 0;
+    if (check_product(atype, n_rows, n_groups, &any, n_cols, depth)) return 0;
+    return moe::expert_backward_workspace(atype, n_rows, n_groups, n_cols, depth);
+}
+
+moe_status_t moe_expert_product_backward(int32_t atype, const void* d_pre_dev, const void* x_dev, const void* w_dev,
+                                         const int32_t* offsets_dev, int32_t n_rows, int32_t n_groups, int32_t n_cols,
+                                         int32_t depth, void* d_x_dev, int32_t d_w_atype, void* d_w_dev,
+                                         void* workspace_dev, size_t workspace_bytes, void* stream) {
+    if (const moe_status_t st = check_product(atype, n_rows, n_groups, offsets_dev, n_cols, depth)) return st;
+    CHECK(d_x_dev || d_w_dev, "nothing to write");
+    CHECK(!d_w_dev || d_w_atype == MOE_A_F32 || d_w_atype == atype, "d_w_atype %d: fp32 or the rows' format", d_w_atype);
+    CHECK(aligned(d_x_dev, 16) && aligned(d_w_dev, 16), "null or misaligned buffer (16 bytes)");
+    if (n_rows == 0 && !d_w_dev) return MOE_OK;
+    CHECK(n_rows == 0 || (!bad(d_pre_dev, 16) && (!d_x_dev || !bad(w_dev, 16)) && (!d_w_dev || !bad(x_dev, 16))),
+          "null or misaligned buffer (16 bytes)");
+    const size_t need = d_w_dev ? moe::expert_backward_workspace(atype, n_rows, n_groups, n_cols, depth) : 0;
+    CHECK(need == 0 || (!bad(workspace_dev, 16) && workspace_bytes >= need), "this gradient needs %zu bytes of workspace", need);
+    const moe::ExpertGradArgs a{d_pre_dev, x_dev, w_dev, offsets_dev, d_x_dev, d_w_dev, static_cast<float*>(workspace_dev),
+                                n_rows, n_groups, n_cols, depth};
+    return launched(moe::launch_expert_backward(atype, d_w_atype, a, static_cast<hipStream_t>(stream)), "expert_product_backward");
 }
 
 }  // extern "C"

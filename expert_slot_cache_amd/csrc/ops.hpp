@@ -1,4 +1,4 @@
-// Launchers of the operators around the experts (router, sorted rows, e4m3 products);
+// Launchers of the operators around the experts (routers, sorted rows, products);
 // C++ linkage, used by ops.cpp only, which checks every argument first.
 #pragma once
 
@@ -16,6 +16,20 @@ hipError_t launch_route(int atype, const void* logits, int64_t stride, int T, in
 hipError_t launch_route_backward(int atype, const void* logits, int64_t stride, const int32_t* ids, const float* w,
                                  const float* dw, int T, int E, int K, bool renorm, void* dlogits, int64_t dstride,
                                  hipStream_t s);
+
+// ---- route_groups.hip ----
+constexpr int kMaxGroups = 64;   // a wave's lanes
+struct RouteGroups {
+    int E, K;
+    int n_groups, kept, group_top;
+    bool sigmoid, renorm;
+    float scale;
+};
+hipError_t launch_route_groups(int atype, const void* logits, int64_t stride, const float* bias, int T,
+                               const RouteGroups& r, int32_t* ids, float* w, hipStream_t s);
+hipError_t launch_route_groups_backward(int atype, const void* logits, int64_t stride, const int32_t* ids, const float* w,
+                                        const float* dw, int T, const RouteGroups& r, void* dlogits, int64_t dstride,
+                                        hipStream_t s);
 
 // ---- rows.hip ----
 // Bytes of the block counts that sorting T*K pairs needs (0: one launch does it all).
@@ -41,5 +55,44 @@ struct ProductArgs {
 };
 enum { OUT_F32 = 0, OUT_BF16 = 1, OUT_SWIGLU = 2 };
 hipError_t launch_scaled_product(const ProductArgs& a, int out, hipStream_t s);
+
+// ---- expert.hip ----
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3, ACT_SWIGLU = 4 };
+struct ExpertArgs {
+    const void* x;            // [M][K]
+    const void* w;            // [G][N][K]
+    const float* bias;        // [G][N] or null
+    const void* resid;        // [M][N or N/2] or null
+    const int32_t* offsets;   // [G+1] or null (G = 1: every row)
+    void* out;                // [M][N or N/2]
+    void* pre;                // [M][N] or null
+    int M, G, N, K, act;
+};
+hipError_t launch_expert_product(int atype, int out_atype, const ExpertArgs& a, hipStream_t s);
+// Bytes of the partial sums of a bias' gradient.
+size_t activation_workspace(int M, int G, int N);
+struct ActivationArgs {
+    const void* dout;         // [M][N or N/2]
+    const void* pre;          // [M][N] or null (ACT_NONE)
+    const int32_t* offsets;
+    void* dpre;               // [M][N] or null
+    float* dbias;             // [G][N] or null
+    float* partial;
+    int M, G, N, act;
+};
+hipError_t launch_activation_backward(int atype, int out_atype, const ActivationArgs& a, hipStream_t s);
+// Bytes of the partial sums of the matrices' gradients (0: none are needed).
+size_t expert_backward_workspace(int atype, int M, int G, int N, int K);
+struct ExpertGradArgs {
+    const void* dpre;         // [M][N]
+    const void* x;            // [M][K], for dw
+    const void* w;            // [G][N][K], for dx
+    const int32_t* offsets;
+    void* dx;                 // [M][K] or null
+    void* dw;                 // [G][N][K] or null
+    float* partial;
+    int M, G, N, K;
+};
+hipError_t launch_expert_backward(int atype, int dw_atype, const ExpertGradArgs& a, hipStream_t s);
 
 }  // namespace moe

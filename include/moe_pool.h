@@ -443,11 +443,12 @@ moe_status_t moe_forward_slots(int32_t wtype, int32_t atype, int32_t hidden, int
                                int32_t n_tokens, void* out_dev, void* stream);
 
 /* ---- the operators around the experts ------------------------------------------ */
-/* A router, tokens sorted by expert and back, and products with 8-bit experts, as calls
- * of their own: what comes before moe_pool_prepare (its topk_ids and gate weights) and,
- * for experts that all live in HBM, the layer in four calls: moe_route, moe_sort_tokens
- * (to e4m3 rows), moe_scaled_product twice, moe_combine_rows.  The router, the sort and
- * the combine have gradients; the products are a serving format, as the INT4 experts are.
+/* Routers, tokens sorted by expert and back, and products with the experts, as calls of
+ * their own: what comes before moe_pool_prepare (its topk_ids and gate weights) and, for
+ * experts that all live in HBM, the layer: moe_route or moe_route_groups, moe_sort_tokens,
+ * moe_expert_product twice (or, of e4m3 rows and experts, moe_scaled_product twice),
+ * moe_combine_rows.  All have gradients but the e4m3 products, a serving format, as the
+ * INT4 experts are.
  *
  * Every call queues its kernels on `stream` (of the current device, where every buffer
  * lives) and returns; none allocates, reads back or keeps anything between calls, so
@@ -484,6 +485,42 @@ moe_status_t moe_route_backward(int32_t atype, const void* logits_dev, int64_t l
                                 const int32_t* topk_ids_dev, const float* topk_w_dev, const float* d_topk_w_dev,
                                 int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t norm, void* d_logits_dev,
                                 int64_t d_logits_stride, void* stream);
+
+/* A router whose choice has a bias for balance and is kept to the best groups of experts
+ * (the experts in n_groups runs of n_experts / n_groups):
+ *   s = the scores: MOE_SCORE_SOFTMAX over all experts, or MOE_SCORE_SIGMOID, 1 / (1 + exp(-l))
+ *   c = s + bias   what experts are chosen by
+ * The kept_groups groups with the largest sum of their group_top (1 or 2) largest c are kept
+ * (equal ones: the lower group); topk_ids are the top_k largest c among their experts, largest
+ * first, equal ones in ascending id order; topk_w = scale s[ids], with MOE_ROUTE_RENORM
+ * scale s[ids] / sum of s[ids].  The bias moves the choice, never a weight.
+ *  logits_dev, topk_ids_dev, topk_w_dev as in moe_route.
+ *  bias_dev      float [n_experts], or NULL: none.
+ *  n_groups      1 (no groups) .. 64, a divisor of n_experts; 1 <= kept_groups <= n_groups;
+ *                top_k <= kept_groups * (n_experts / n_groups).
+ *  scale         finite and above 0.
+ * Choices are compared as in fp64 (without a bias experts are compared by their logits).  An
+ * expert whose logit or bias is -inf or NaN is masked: it is chosen only when nothing else is
+ * left in the kept groups (in ascending id order), does not count in its group's sum, and a
+ * group of masked experts alone is kept only when no other is left; the score of a logit of -inf
+ * or NaN is 0.  Weights whose sum is 0 are 0.  Errors: EINVAL, EHIP. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+moe_status_t moe_route_groups(int32_t atype, const void* logits_dev, int64_t logits_stride, const float* bias_dev,
+                              int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t score, int32_t norm,
+                              int32_t n_groups, int32_t kept_groups, int32_t group_top, float scale,
+                              int32_t* topk_ids_dev, float* topk_w_dev, void* stream);
+/* Its gradient (the choice has none, and neither has the bias): from d_topk_w_dev float
+ * [n_tokens][top_k] and the call's ids and weights, d_logits_dev as in moe_route_backward.  With
+ * S = sum_k w_k dw_k and g_e the sum of the dw of e:
+ *   softmax:  dl_e = s_e (scale g_e - S);       RENORM: the sum over the k of e of w_k (dw_k - S / scale)
+ *   sigmoid:  the sum over the k of e of w_k (1 - s_e) dw_k;   RENORM: of w_k (1 - s_e) (dw_k - S / scale)
+ * Softmax with RENORM does not read logits_dev (it may be NULL).  An id outside [0, n_experts)
+ * contributes nothing.  Errors: EINVAL, EHIP. */
+moe_status_t moe_route_groups_backward(int32_t atype, const void* logits_dev, int64_t logits_stride,
+                                       const int32_t* topk_ids_dev, const float* topk_w_dev, const float* d_topk_w_dev,
+                                       int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t score, int32_t norm,
+                                       float scale, void* d_logits_dev, int64_t d_logits_stride, void* stream);
 
 /* Tokens to one row per (token, k) pair, sorted by expert: the pairs whose id lies in
  * [0, n_experts), by id and then by (token, k).  Pairs with any other id (padding tokens:
@@ -555,6 +592,71 @@ moe_status_t moe_scaled_product(const void* x_dev, const float* x_scales_dev, co
                                 const float* w_scales_dev, const int32_t* offsets_dev, int32_t n_rows,
                                 int32_t n_groups, int32_t n_cols, int32_t depth, int32_t epilogue, void* out_dev,
                                 float* out_scales_dev, void* stream);
+
+/* Sorted rows times their group's matrix in the activation format, with bias, activation and
+ * residual in the epilogue; group g has the rows offsets[g] .. offsets[g+1]:
+ *   h = x[r] w[g]^T + bias[g],   out[r] = act(h) + resid[r]
+ * Products of bf16 values are exact; sums are fp32, and each output is rounded once from them.
+ *  x_dev         [n_rows][depth] and w_dev [n_groups][n_cols][depth] in the activation format;
+ *                n_cols and depth multiples of 8 (fp32: 4); n_rows <= 2^24, at most 2^36 elements
+ *                in w_dev and in any array of rows.
+ *  bias_dev      float [n_groups][n_cols], or NULL: none.
+ *  offsets_dev   int32 [n_groups + 1], rising within [0, n_rows], or NULL for one group of all n_rows
+ *                rows.  With others no memory outside the buffers is touched, but what the outputs
+ *                then hold is not defined.
+ *  act           MOE_ACT_NONE; _RELU; _GELU, h times the normal distribution function of h; _SILU,
+ *                h / (1 + exp(-h)); _SWIGLU (n_cols a multiple of 16, fp32: 8): columns [0, n_cols/2)
+ *                are the gate, the rest the up projection: silu(gate) * up, n_cols/2 outputs a row.
+ *  out_dev       [n_rows][n_cols (SwiGLU: n_cols/2)] in out_atype, fp32 or the activation format;
+ *  resid_dev     the same, or NULL: none.  It may be out_dev itself.
+ *  pre_dev       [n_rows][n_cols] in the activation format, written: h (for the gradient); or NULL.
+ * Buffers on 16 bytes but for bias_dev and offsets_dev.  Rows outside every group are left as
+ * they are.  Errors: EINVAL, EHIP. */
+#define MOE_ACT_NONE   0
+#define MOE_ACT_RELU   1
+#define MOE_ACT_GELU   2
+#define MOE_ACT_SILU   3
+#define MOE_ACT_SWIGLU 4
+moe_status_t moe_expert_product(int32_t atype, const void* x_dev, const void* w_dev, const float* bias_dev,
+                                const int32_t* offsets_dev, const void* resid_dev, int32_t n_rows, int32_t n_groups,
+                                int32_t n_cols, int32_t depth, int32_t act, int32_t out_atype, void* out_dev,
+                                void* pre_dev, void* stream);
+/* Its gradient, in two calls.  First back through the epilogue (the residual's gradient is d_out
+ * itself):
+ *   d_pre[r] = d_out[r] act'(pre[r]),   d_bias[g] = the sum of the group's d_pre (unrounded, fp32)
+ *  d_out_dev     [n_rows][n_cols (SwiGLU: n_cols/2)] in out_atype; pre_dev and d_pre_dev [n_rows]
+ *                [n_cols] in the activation format (MOE_ACT_NONE: pre_dev is not read, and d_pre
+ *                is d_out in that format); d_bias_dev float [n_groups][n_cols].  d_pre_dev or
+ *                d_bias_dev may be NULL: not wanted.  d_pre_dev may be pre_dev, and with
+ *                MOE_ACT_NONE in the same format d_out_dev.
+ *  workspace_dev moe_activation_backward_workspace_bytes(n_rows, n_groups, n_cols) bytes on 16
+ *                where d_bias_dev is given, used by this call only.
+ * A group without rows has a d_bias of 0 (n_rows = 0 as well).  Sizes, offsets, alignment and the
+ * rows outside every group as in moe_expert_product.  Errors: EINVAL, EHIP. */
+moe_status_t moe_activation_backward(int32_t atype, const void* d_out_dev, int32_t out_atype, const void* pre_dev,
+                                     const int32_t* offsets_dev, int32_t n_rows, int32_t n_groups, int32_t n_cols,
+                                     int32_t act, void* d_pre_dev, float* d_bias_dev, void* workspace_dev,
+                                     size_t workspace_bytes, void* stream);
+/* Bytes of that workspace (0 also for sizes that moe_activation_backward refuses). */
+size_t moe_activation_backward_workspace_bytes(int32_t n_rows, int32_t n_groups, int32_t n_cols);
+/* Then back through the product:
+ *   d_x[r] = d_pre[r] w[g],   d_w[g] = the sum over the group's rows of d_pre[r]^T x[r]
+ *  d_pre_dev     [n_rows][n_cols], x_dev [n_rows][depth] and w_dev [n_groups][n_cols][depth] in the
+ *                activation format; x_dev is read for d_w alone and w_dev for d_x alone.
+ *  d_x_dev       [n_rows][depth] in the activation format, or NULL: not wanted.
+ *  d_w_dev       [n_groups][n_cols][depth] in d_w_atype, fp32 or the activation format, or NULL.
+ *                A group without rows has a d_w of 0 (n_rows = 0 as well).
+ *  workspace_dev moe_expert_product_backward_workspace_bytes(atype, n_rows, n_groups, n_cols, depth)
+ *                bytes on 16 (0: none) where d_w_dev is given, used by this call only.
+ * Sizes, offsets, alignment, sums and the rows outside every group as in moe_expert_product.
+ * Errors: EINVAL, EHIP. */
+moe_status_t moe_expert_product_backward(int32_t atype, const void* d_pre_dev, const void* x_dev, const void* w_dev,
+                                         const int32_t* offsets_dev, int32_t n_rows, int32_t n_groups, int32_t n_cols,
+                                         int32_t depth, void* d_x_dev, int32_t d_w_atype, void* d_w_dev,
+                                         void* workspace_dev, size_t workspace_bytes, void* stream);
+/* Bytes of that workspace (0 also for sizes that moe_expert_product_backward refuses). */
+size_t moe_expert_product_backward_workspace_bytes(int32_t atype, int32_t n_rows, int32_t n_groups, int32_t n_cols,
+                                                   int32_t depth);
 
 /* ---- the slot manager alone (host only, no GPU) ----------------------------- */
 /* The same per-layer LRU state machine prepare() runs, driven from host ids, for
