@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_pool.so")
 
 SOURCES = ["kernels.hip", "fill.hip", "policy.hip", "calibrate.hip", "moe_pool.cpp", "noalloc.cpp",
-           "route.hip", "route_groups.hip", "rows.hip", "scaled.hip", "expert.hip", "ops.cpp"]
+           "route.hip", "route_groups.hip", "rows.hip", "scaled.hip", "expert.hip", "expert_backward.hip",
+           "activation.hip", "ops.cpp"]
 ARCH = "gfx950"
 
 # Every HIP compile disables packed fp32 instructions (v_pk_*_f32).

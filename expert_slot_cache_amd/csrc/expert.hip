@@ -1,268 +1,101 @@
-// The products of sorted rows with their expert's matrix in the activation format, and their
-// gradients.  For the rows r of group g (offsets[g] <= r < offsets[g+1]):
+// The product of sorted rows with their group's matrix in the activation format, with bias,
+// activation and residual in the epilogue.  For the rows r of group g (offsets[g] <= r < offsets[g+1]):
 //
 //   h = x[r] w[g]^T + bias[g],  out = act(h) + resid[r]          (pre = h)
-//   d_pre = d_out act'(pre),    d_bias[g] = sum_r d_pre[r]
-//   d_x[r] = d_pre[r] w[g],     d_w[g] = sum_r d_pre[r] x[r]^T
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
-#include "ops.hpp"
-#include "ops_dev.hpp"
+#include "expert_act.hpp"
+#include "expert_core.hpp"
+#include "product_tile.hpp"
 #include "works.hpp"
 
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float sigmoid(float h) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(h * -1.44269504f));
-}
-// The distribution function of the normal distribution.
-__device__ __forceinline__ float normal_cdf(float h) { return 0.5f * erfcf(h * -0.70710678f); }
+template <class C, int AT, bool GATED>
+__global__ __launch_bounds__(64 * C::WAVES) void k_expert(ExpertArgs p, int out_at, int nblocks) {
+    constexpr int F = C::F, FA = C::FA, FB = C::FB, ES = AT == A_F32 ? 4 : 2;
+    constexpr int COLS = GATED ? C::PA / 2 : C::PA, HF = GATED ? FA / 2 : FA;
+    __shared__ __align__(1024) char lds[kCoreLds<C>];
+    const Works<C::PB> works(p.offsets, p.G, p.M, nblocks);
+    // workgroup b runs on XCD b % 8: each XCD takes one contiguous run of the work
+    const int per = (works.total + 7) >> 3;
+    const int jx = (int)(blockIdx.x >> 3);
+    const int wk = (int)(blockIdx.x & 7) * per + jx;
+    if (jx >= per || wk >= works.total) return;
+    const Work tl = works.at(wk);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wa = wave % C::WA, wb = wave / C::WA;
+    const int N = p.N, K = p.K, width = GATED ? N / 2 : N, n0 = tl.nb * COLS;
+    const uint32_t pitch = (uint32_t)K * ES;
+    const char* w = static_cast<const char*>(p.w) + ((size_t)tl.group * N + n0) * pitch;
+    const Operand a{w, pitch, min(COLS, width - n0), (int)pitch};
+    const Operand up{w + (size_t)(GATED ? width : 0) * pitch, pitch, a.rows, a.depth};
+    const Operand b{static_cast<const char*>(p.x) + (size_t)tl.row0 * pitch, pitch, tl.rows, (int)pitch};
+    Sums<F> acc[FA][FB];
+    const bool live = wb * F * FB < tl.rows;
+    core<C, AT, false, false, GATED>(lds, a, up, b, live, acc);
 
-__device__ __forceinline__ float activate(int act, float h) {
-    if (act == ACT_RELU) return h > 0.0f ? h : 0.0f;
-    if (act == ACT_GELU) return h * normal_cdf(h);
-    if (act == ACT_SILU) return h * sigmoid(h);
-    return h;
-}
-__device__ __forceinline__ float slope(int act, float h) {
-    if (act == ACT_RELU) return h > 0.0f ? 1.0f : 0.0f;
-    if (act == ACT_GELU) return normal_cdf(h) + h * 0.39894228f * __builtin_amdgcn_exp2f(h * h * -0.72134752f);
-    if (act == ACT_SILU) {
-        const float s = sigmoid(h);
-        return s * (1.0f + h * (1.0f - s));
+    const int c0 = n0 + wa * HF * F, r0 = tl.row0 + wb * FB * F;     // of the wave's part
+    const int lanes_c = c0 + (int)(threadIdx.x & 63) % (HF * F / 8) * 8;
+    const bool here = lanes_c < width, whole = lanes_c + 8 <= width;
+    float bias[8], up_bias[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float* from = p.bias + (size_t)tl.group * N + lanes_c + i;
+        const bool there = p.bias && lanes_c + i < width;
+        bias[i] = there ? from[0] : 0.0f;
+        up_bias[i] = GATED && there ? from[width] : 0.0f;
     }
-    return 1.0f;
-}
-
-enum { FORWARD, ROWS, MATRICES };
-
-// A workgroup computes 64 x 64 outputs, a thread 4 x 4 of them, 16 apart: i of the rows (or, of a
-// matrix' gradient, of its rows), j of the columns.
-template <int MODE, int AT, int OT>
-__global__ __launch_bounds__(256) void k_simple(const void* __restrict__ a, const void* __restrict__ b, ExpertArgs p,
-                                                int nblocks) {
-    __shared__ float as[16][65], bs[16][65];
-    const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
-    const int M = p.M, N = p.N, K = p.K;
-    int group, row0, rows, nb, r0 = 0, depth;              // depth: what is summed over
-    if (MODE == MATRICES) {
-        group = blockIdx.z;
-        row0 = blockIdx.y * 64;
-        rows = min(64, N - row0);
-        nb = blockIdx.x;
-        int hi = M;
-        if (p.offsets) {
-            r0 = min(max(p.offsets[group], 0), M);
-            hi = min(max(p.offsets[group + 1], r0), M);
-        }
-        depth = hi - r0;
-    } else {
-        const Works<64> works(p.offsets, p.G, M, nblocks);
-        if ((int)blockIdx.x >= works.total) return;
-        const Work tl = works.at(blockIdx.x);
-        group = tl.group, row0 = tl.row0, rows = tl.rows, nb = tl.nb;
-        depth = MODE == FORWARD ? K : N;
-    }
-    const bool gated = MODE == FORWARD && p.act == ACT_SWIGLU;
-    const int half = N / 2, cols = MODE == FORWARD ? (gated ? half : N) : K;
-    const size_t wg = (size_t)group * N * K;
-    auto column = [&](int c) {                             // of the tile's column c: where it is, or -1
-        if (gated) {
-            const int n = nb * 32 + (c & 31);
-            return n < half ? n + (c >> 5) * half : -1;
-        }
-        return nb * 64 + c < cols ? nb * 64 + c : -1;
-    };
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < depth; k0 += 16) {
-        for (int e = tid; e < 1024; e += 256) {
-            const int k = MODE == MATRICES ? e >> 6 : e & 15, i = MODE == MATRICES ? e & 63 : e >> 4;
-            float v = 0.0f;
-            if (i < rows && k0 + k < depth) {
-                if (MODE == FORWARD) v = load_one<AT>(a, (size_t)(row0 + i) * K + k0 + k);
-                else if (MODE == ROWS) v = load_one<AT>(a, (size_t)(row0 + i) * N + k0 + k);
-                else v = load_one<AT>(a, (size_t)(r0 + k0 + k) * N + row0 + i);
-            }
-            as[k][i] = v;
-            const int kb = MODE == FORWARD ? e & 15 : e >> 6, j = MODE == FORWARD ? e >> 4 : e & 63;
-            const int n = column(j);
-            v = 0.0f;
-            if (n >= 0 && k0 + kb < depth) {
-                if (MODE == FORWARD) v = load_one<AT>(b, wg + (size_t)n * K + k0 + kb);
-                else if (MODE == ROWS) v = load_one<AT>(b, wg + (size_t)(k0 + kb) * K + n);
-                else v = load_one<AT>(b, (size_t)(r0 + k0 + kb) * K + n);
-            }
-            bs[kb][j] = v;
-        }
-        __syncthreads();
-        for (int k = 0; k < 16; ++k) {
-            float av[4], bv[4];
-            for (int q = 0; q < 4; ++q) av[q] = as[k][ti + 16 * q], bv[q] = bs[k][tj + 16 * q];
+    each_run<C, GATED>(lds, acc, tl.rows - wb * FB * F, [&](int r, int c, float* v, float* up) {
+        if (!here) return;
+        const size_t row = r0 + r, n = c0 + c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i) v[i] += bias[i];
+        if (p.pre) store8<AT>(p.pre, row * N + n, whole, v);
+        if constexpr (GATED) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += av[i] * bv[j];
+            for (int i = 0; i < 8; ++i) up[i] += up_bias[i];
+            if (p.pre) store8<AT>(p.pre, row * N + width + n, whole, up);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid(v[i]) * up[i];
+        } else if (p.act != ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = activate(p.act, v[i]);
         }
-        __syncthreads();
-    }
+        const size_t at = row * width + n;
+        if (p.resid) {
+            float more[8];
+            if (AT == A_F32 || out_at == A_F32) load8<A_F32>(p.resid, at, whole, more);
+            else load8<A_BF16>(p.resid, at, whole, more);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (ti + 16 * i >= rows) continue;
-        const size_t r = row0 + ti + 16 * i;
-        if (MODE != FORWARD) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = column(tj + 16 * j);
-                if (n >= 0) store_one<OT>(p.out, (MODE == MATRICES ? wg : 0) + r * K + n, acc[i][j]);
-            }
-            continue;
+            for (int i = 0; i < 8; ++i) v[i] += more[i];
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = column(tj + 16 * j);
-            if (n < 0) continue;
-            if (p.bias) acc[i][j] += p.bias[(size_t)group * N + n];
-            if (p.pre) store_one<AT>(p.pre, r * N + n, acc[i][j]);
-            if (gated) continue;
-            const float v = activate(p.act, acc[i][j]);
-            store_one<OT>(p.out, r * N + n, v + (p.resid ? load_one<OT>(p.resid, r * N + n) : 0.0f));
-        }
-        if (gated)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int n = column(tj + 16 * j);
-                if (n < 0) continue;
-                const float v = acc[i][j] * sigmoid(acc[i][j]) * acc[i][j + 2];
-                store_one<OT>(p.out, r * half + n, v + (p.resid ? load_one<OT>(p.resid, r * half + n) : 0.0f));
-            }
-    }
+        store8_as<AT>(out_at, p.out, at, whole, v);
+    });
 }
 
-// ---- the gradient before the activation ------------------------------------------------------
-
-constexpr int kActRows = 64;   // rows of a partial sum
-
-// A thread takes a column of up to 64 rows of a group; their sum goes to the place of the tile,
-// which no other has: row0 / 64 + group rises by one at least from a tile to the next.
-template <int AT, int OT>
-__global__ __launch_bounds__(256) void k_activation_backward(ActivationArgs p, int nblocks) {
-    const Works<kActRows> works(p.offsets, p.G, p.M, nblocks);
-    if ((int)blockIdx.x >= works.total) return;
-    const Work tl = works.at(blockIdx.x);
-    const bool gated = p.act == ACT_SWIGLU;
-    const int half = p.N / 2, n = tl.nb * 256 + threadIdx.x;
-    if (n >= (gated ? half : p.N)) return;
-    float sum = 0.0f, up_sum = 0.0f;
-    for (int i = 0; i < tl.rows; ++i) {
-        const size_t r = tl.row0 + i;
-        if (gated) {
-            const float d = load_one<OT>(p.dout, r * half + n);
-            const float g = load_one<AT>(p.pre, r * p.N + n), u = load_one<AT>(p.pre, r * p.N + half + n);
-            const float dg = d * u * slope(ACT_SILU, g), du = d * g * sigmoid(g);
-            sum += dg;
-            up_sum += du;
-            if (p.dpre) {
-                store_one<AT>(p.dpre, r * p.N + n, dg);
-                store_one<AT>(p.dpre, r * p.N + half + n, du);
-            }
-        } else {
-            float d = load_one<OT>(p.dout, r * p.N + n);
-            if (p.act != ACT_NONE) d *= slope(p.act, load_one<AT>(p.pre, r * p.N + n));
-            sum += d;
-            if (p.dpre) store_one<AT>(p.dpre, r * p.N + n, d);
-        }
-    }
-    if (p.dbias) {
-        float* to = p.partial + (size_t)(tl.row0 / kActRows + tl.group) * p.N + n;
-        to[0] = sum;
-        if (gated) to[half] = up_sum;
-    }
-}
-
-__global__ __launch_bounds__(256) void k_bias_sums(ActivationArgs p) {
-    const int n = blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
-    if (n >= p.N) return;
-    int lo = 0, hi = p.M;
-    if (p.offsets) {
-        // as the works bound them: falling offsets count as the largest before them
-        for (int i = 0; i <= g; ++i) lo = min(max(p.offsets[i], lo), p.M);
-        hi = min(max(p.offsets[g + 1], lo), p.M);
-    }
-    const int tiles = (hi - lo + kActRows - 1) / kActRows;
-    const float* from = p.partial + (size_t)(lo / kActRows + g) * p.N + n;
-    float sum = 0.0f;
-    for (int i = 0; i < tiles; ++i) sum += from[(size_t)i * p.N];
-    p.dbias[(size_t)g * p.N + n] = sum;
-}
-
-// Tiles of 64 rows that M rows of G groups can have.
-int64_t most(int64_t M, int64_t G, bool offsets) { return offsets ? M / 64 + (G < M ? G : M) : (M + 63) / 64; }
-
-template <int MODE, int AT, int OT>
-hipError_t simple(const void* a, const void* b, const ExpertArgs& p, hipStream_t s) {
-    const int cols = MODE != FORWARD ? p.K : p.act == ACT_SWIGLU ? p.N : (p.N + 63) / 64 * 64;
-    const int nblocks = (cols + 63) / 64;
-    if (MODE == MATRICES) {
-        hipLaunchKernelGGL((k_simple<MODE, AT, OT>), dim3(nblocks, (p.N + 63) / 64, p.G), dim3(256), 0, s, a, b, p, nblocks);
-    } else {
-        hipLaunchKernelGGL((k_simple<MODE, AT, OT>), dim3((unsigned)(nblocks * most(p.M, p.G, p.offsets))), dim3(256), 0, s, a,
-                           b, p, nblocks);
-    }
+template <class C, int AT, bool GATED>
+hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
+    constexpr int COLS = GATED ? C::PA / 2 : C::PA;
+    const int nblocks = ((GATED ? p.N / 2 : p.N) + COLS - 1) / COLS;
+    const int64_t grid = (nblocks * most_tiles(p.M, p.G, p.offsets, C::PB) + 7) / 8 * 8;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_expert<C, AT, GATED>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, p, out_at, nblocks);
     return hipGetLastError();
 }
 
-// f of the two formats as constants (the second is fp32 or the first).
-template <class F>
-hipError_t by_types(int at, int ot, F f) {
-    typedef std::integral_constant<int, A_F32> F32;
-    typedef std::integral_constant<int, A_BF16> BF16;
-    if (at == A_F32) return f(F32{}, F32{});
-    return ot == A_F32 ? f(BF16{}, F32{}) : f(BF16{}, BF16{});
+template <int AT, bool GATED>
+hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
+    return expert_tile(p.M, p.G, p.N, p.offsets, [&](auto tile) { return expert<decltype(tile), AT, GATED>(p, out_at, s); });
 }
 
 }  // namespace
 
-hipError_t launch_expert_product(int atype, int out_atype, const ExpertArgs& a, hipStream_t s) {
-    return by_types(atype, out_atype, [&](auto at, auto ot) {
-        return simple<FORWARD, decltype(at)::value, decltype(ot)::value>(a.x, a.w, a, s);
-    });
-}
-
-size_t activation_workspace(int M, int G, int N) { return (size_t)(M / kActRows + G) * N * sizeof(float); }
-
-hipError_t launch_activation_backward(int atype, int out_atype, const ActivationArgs& a, hipStream_t s) {
-    return by_types(atype, out_atype, [&](auto at, auto ot) {
-        const int nblocks = ((a.act == ACT_SWIGLU ? a.N / 2 : a.N) + 255) / 256;
-        if (a.M > 0) {
-            hipLaunchKernelGGL((k_activation_backward<decltype(at)::value, decltype(ot)::value>),
-                               dim3((unsigned)(nblocks * most(a.M, a.G, a.offsets))), dim3(256), 0, s, a, nblocks);
-            if (const hipError_t e = hipGetLastError()) return e;
-        }
-        if (a.dbias) hipLaunchKernelGGL(k_bias_sums, dim3((a.N + 255) / 256, a.G), dim3(256), 0, s, a);
-        return hipGetLastError();
-    });
-}
-
-size_t expert_backward_workspace(int atype, int M, int G, int N, int K) { return 0; }
-
-hipError_t launch_expert_backward(int atype, int dw_atype, const ExpertGradArgs& g, hipStream_t s) {
-    ExpertArgs a{};
-    a.offsets = g.offsets;
-    a.M = g.M, a.G = g.G, a.N = g.N, a.K = g.K;
-    if (g.dx && g.M > 0) {
-        a.out = g.dx;
-        const hipError_t e = atype == A_F32 ? simple<ROWS, A_F32, A_F32>(g.dpre, g.w, a, s)
-                                            : simple<ROWS, A_BF16, A_BF16>(g.dpre, g.w, a, s);
-        if (e) return e;
-    }
-    if (!g.dw) return hipSuccess;
-    a.out = g.dw;
-    return by_types(atype, dw_atype, [&](auto at, auto ot) {
-        return simple<MATRICES, decltype(at)::value, decltype(ot)::value>(g.dpre, g.x, a, s);
-    });
+hipError_t launch_expert_product(int atype, int out_atype, const ExpertArgs& p, hipStream_t s) {
+    const bool gated = p.act == ACT_SWIGLU;
+    if (atype == A_F32) return gated ? expert<A_F32, true>(p, out_atype, s) : expert<A_F32, false>(p, out_atype, s);
+    return gated ? expert<A_BF16, true>(p, out_atype, s) : expert<A_BF16, false>(p, out_atype, s);
 }
 
 }  // namespace moe

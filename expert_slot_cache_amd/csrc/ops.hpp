@@ -5,6 +5,9 @@
 #include <hip/hip_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <type_traits>
+
+#include "kernels.hpp"
 
 namespace moe {
 
@@ -56,6 +59,15 @@ struct ProductArgs {
 enum { OUT_F32 = 0, OUT_BF16 = 1, OUT_SWIGLU = 2 };
 hipError_t launch_scaled_product(const ProductArgs& a, int out, hipStream_t s);
 
+// f of two formats as constants (the second is fp32 or the first).
+template <class F>
+hipError_t by_types(int at, int ot, F f) {
+    typedef std::integral_constant<int, A_F32> F32;
+    typedef std::integral_constant<int, A_BF16> BF16;
+    if (at == A_F32) return f(F32{}, F32{});
+    return ot == A_F32 ? f(BF16{}, F32{}) : f(BF16{}, BF16{});
+}
+
 // ---- expert.hip ----
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3, ACT_SWIGLU = 4 };
 struct ExpertArgs {
@@ -69,6 +81,8 @@ struct ExpertArgs {
     int M, G, N, K, act;
 };
 hipError_t launch_expert_product(int atype, int out_atype, const ExpertArgs& a, hipStream_t s);
+
+// ---- activation.hip ----
 // Bytes of the partial sums of a bias' gradient.
 size_t activation_workspace(int M, int G, int N);
 struct ActivationArgs {
@@ -81,6 +95,8 @@ struct ActivationArgs {
     int M, G, N, act;
 };
 hipError_t launch_activation_backward(int atype, int out_atype, const ActivationArgs& a, hipStream_t s);
+
+// ---- expert_backward.hip ----
 // Bytes of the partial sums of the matrices' gradients (0: none are needed).
 size_t expert_backward_workspace(int atype, int M, int G, int N, int K);
 struct ExpertGradArgs {

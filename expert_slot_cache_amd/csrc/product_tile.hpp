@@ -48,4 +48,48 @@ auto product_tile(int64_t M, int64_t G, int64_t N, bool offsets, F f) {
     }
 }
 
+// ---- products in the activation format ----
+//
+// A workgroup of WA x WB waves computes PA columns x PB rows of the output, in fragments of F x F
+// (the columns are the instruction's A operand, so that four accumulators of a lane are consecutive
+// columns).  A stage of the ring holds RB bytes of the summed dimension of each of them; S stages.
+template <int PA_, int PB_, int WA_, int WB_, int F_, int RB_, int S_>
+struct CoreTile {
+    static constexpr int PA = PA_, PB = PB_, WA = WA_, WB = WB_, F = F_, RB = RB_, S = S_;
+    static constexpr int WAVES = WA * WB, FA = PA / WA / F, FB = PB / WB / F;
+    static constexpr int ROWS = 1024 / RB;                // rows of a copy (1024 bytes, 16 a lane)
+    static constexpr int CA = PA * RB / 1024, CB = PB * RB / 1024;   // copies of a stage,
+    static constexpr int NA = CA / WAVES, NB = CB / WAVES;           // a wave's (NB 0: the first CB waves have one)
+    static constexpr int STAGE = (PA + PB) * RB, LDS = S * STAGE;
+    static_assert(FA >= 1 && FB >= 1 && NA >= 1 && NA * WAVES == CA && (NB > 0 ? NB * WAVES == CB : CB < WAVES), "");
+    static_assert(S >= 2 && LDS <= 160 * 1024 && (RB == 128 || (RB == 64 && F == 32)), "");
+};
+
+template <class F>
+auto expert_tile(int64_t M, int64_t G, int64_t N, bool offsets, F f) {
+    const int64_t avg = M / G;
+    auto fills = [&](int PA, int PB, int64_t least) { return (N + PA - 1) / PA * most_tiles(M, G, offsets, PB) >= least; };
+    constexpr int64_t kMost = 192;
+    if (avg >= 64 && fills(256, 256, kMost)) return f(CoreTile<256, 256, 2, 4, 32, 64, 4>{});
+    if (avg >= 32 && fills(128, 128, kMost)) return f(CoreTile<128, 128, 2, 2, 32, 128, 3>{});
+    if (avg < 16 && fills(128, 16, kMost)) return f(CoreTile<128, 16, 4, 1, 16, 128, 4>{});
+    if (avg >= 16 && fills(64, 64, 128)) return f(CoreTile<64, 64, 1, 2, 32, 128, 4>{});
+    return f(CoreTile<32, 16, 1, 1, 16, 128, 8>{});
+}
+
+// f of the tile of a matrix' gradient, and the parts that its rows are split into.
+template <class F>
+auto matrix_tile(int64_t M, int64_t G, int64_t N, int64_t K, F f) {
+    auto splits = [&](int PA, int PB) {
+        const int64_t tiles = G * ((K + PA - 1) / PA) * ((N + PB - 1) / PB);
+        int64_t n = (384 + tiles - 1) / tiles;
+        const int64_t most = M / G / 512;
+        if (n > most) n = most;
+        return (int)(n > 1 ? n : 1);
+    };
+    if (N >= 192 && K >= 192 && G * ((K + 255) / 256) * ((N + 255) / 256) >= 192)
+        return f(CoreTile<256, 256, 2, 4, 32, 64, 4>{}, 1);
+    return f(CoreTile<128, 64, 2, 2, 32, 128, 4>{}, splits(128, 64));
+}
+
 }  // namespace moe
