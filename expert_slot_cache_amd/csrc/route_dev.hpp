@@ -60,6 +60,17 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+template <int L>
+__device__ __forceinline__ uint32_t lanes_or(uint32_t v) {
+    if constexpr (L == 64) return wave_reduce_u32(v, [](uint32_t a, uint32_t b) { return a | b; });
+    auto turn = [&](auto ctrl) { v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xf, 0xf, false); };
+    turn(std::integral_constant<int, 0x128>{});
+    turn(std::integral_constant<int, 0x124>{});
+    turn(std::integral_constant<int, 0x122>{});
+    turn(std::integral_constant<int, 0x121>{});
+    return v;
+}
+
 // A lane's V keys in eights, each in descending order, and (NAMES) the places its keys had.
 template <int V, bool NAMES>
 struct Eights {
