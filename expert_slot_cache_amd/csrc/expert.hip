@@ -32,14 +32,10 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_expert(ExpertArgs p, int out_
     const Operand a{w, pitch, min(COLS, width - n0), (int)pitch};
     const Operand up{w + (size_t)(GATED ? width : 0) * pitch, pitch, a.rows, a.depth};
     const Operand b{static_cast<const char*>(p.x) + (size_t)tl.row0 * pitch, pitch, tl.rows, (int)pitch};
-    Sums<F> acc[FA][FB];
-    const bool live = wb * F * FB < tl.rows;
-    core<C, AT, false, false, GATED>(lds, a, up, b, live, acc);
-
     const int c0 = n0 + wa * HF * F, r0 = tl.row0 + wb * FB * F;     // of the wave's part
     const int lanes_c = c0 + (int)(threadIdx.x & 63) % (HF * F / 8) * 8;
     const bool here = lanes_c < width, whole = lanes_c + 8 <= width;
-    float bias[8], up_bias[8];
+    float bias[8], up_bias[8];                             // requested ahead of the tile's copies
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float* from = p.bias + (size_t)tl.group * N + lanes_c + i;
@@ -47,6 +43,10 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_expert(ExpertArgs p, int out_
         bias[i] = there ? from[0] : 0.0f;
         up_bias[i] = GATED && there ? from[width] : 0.0f;
     }
+    Sums<F> acc[FA][FB];
+    const bool live = wb * F * FB < tl.rows;
+    core<C, AT, false, false, GATED>(lds, a, up, b, live, acc);
+
     each_run<C, GATED>(lds, acc, tl.rows - wb * FB * F, [&](int r, int c, float* v, float* up) {
         if (!here) return;
         const size_t row = r0 + r, n = c0 + c;
@@ -87,7 +87,7 @@ hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
 
 template <int AT, bool GATED>
 hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
-    return expert_tile(p.M, p.G, p.N, p.offsets, [&](auto tile) { return expert<decltype(tile), AT, GATED>(p, out_at, s); });
+    return expert_tile(AT == A_BF16, p.M, p.G, p.N, p.offsets, [&](auto tile) { return expert<decltype(tile), AT, GATED>(p, out_at, s); });
 }
 
 }  // namespace

@@ -58,7 +58,7 @@ struct Side {
     static constexpr int KK = DEPTH / STEP;
     static __device__ __forceinline__ int turn(int row) {  // what a row's chunks are exchanged by
         if (ACROSS) return AT == A_F32 ? 0 : P >= 128 ? row & 3 : P == 64 ? (row >> 1) & 1 : 0;
-        return RB == 128 ? row & 7 : (row >> 1) & 3;
+        return RB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
     }
     // What lane `lane` of copy number c takes: offset from the stage's base.
     static __device__ __forceinline__ uint32_t source(int c, int lane, uint32_t pitch) {
@@ -174,55 +174,46 @@ __device__ __forceinline__ void core(char* lds, const Operand& a, const Operand&
         boff[i] = SB::source(c, lane, b.pitch);
         if constexpr (!TB) boff[i] += (c * C::ROWS + lane / (C::RB / 16)) * b.pitch;
     }
-    // In the last, shorter stage an along row's chunks past its end are zeros; across, the rows are.
+    // In the last, shorter stage an along row's chunks past its end are zeros; across, the rows are.  A
+    // stage behind the last is all zeros: nothing is read for it, and it keeps the count of copies.
     auto bytes = [&](const Operand& o, bool across, int st) -> uint32_t {
+        if (st >= stages) return 0;
         if (across) return (uint32_t)(min(DEPTH, o.depth - st * DEPTH) - 1) * o.pitch + o.rows;
         return (uint32_t)o.rows * o.pitch - st * C::RB;
     };
-    auto base = [&](const Operand& o, bool across, int st) {
-        return o.base + (across ? (size_t)st * DEPTH * o.pitch : (size_t)st * C::RB);
+    auto buffer = [&](const Operand& o, bool across, int st) {
+        return buffer_of(o.base + (across ? (size_t)st * DEPTH * o.pitch : (size_t)st * C::RB), bytes(o, across, st));
     };
-    auto past = [&](int c, bool across) {                  // of the last stage, this lane's chunk lies past the end
-        if (across) return false;
+    auto past = [&](int c) {                               // this lane's chunk of an along row lies past the end
         const int row = c * C::ROWS + lane / (C::RB / 16);
-        return ((lane % (C::RB / 16)) ^ (C::RB == 128 ? row & 7 : (row >> 1) & 3)) * 16 >= tail;
+        return ((lane % (C::RB / 16)) ^ Side<C, AT, false, C::PA>::turn(row)) * 16 >= tail;
     };
-    auto fill = [&](int st, int stage) {
-        const uint32_t at = lds0 + stage * C::STAGE;
-        const bool last = st == stages - 1;
-        const i32x4_t ba = buffer_of(base(a, TA, st), bytes(a, TA, st)), bb = buffer_of(base(b, TB, st), bytes(b, TB, st));
-        i32x4_t bu = ba;
-        if constexpr (GATED) bu = buffer_of(base(up, false, st), bytes(up, false, st));
-#pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int c = wave + WAVES * i;
-            uint32_t off = aoff[i];
-            if (!TA && last && past(c, false)) off = kPastEnd;
-            if (GATED && c * C::ROWS / F % FA >= FA / 2) copy_bounded(at + c * 1024, off, bu);
-            else copy_bounded(at + c * 1024, off, ba);
-        }
-        if (has_b)
-#pragma unroll
-            for (int i = 0; i < NB1; ++i) {
-                const int c = wave + WAVES * i;
-                uint32_t off = boff[i];
-                if (!TB && last && past(c, false)) off = kPastEnd;
-                copy_bounded(at + C::PA * C::RB + c * 1024, off, bb);
-            }
+    i32x4_t ba, bu, bb;
+    uint32_t to;
+    bool last;
+    auto refill = [&](int st, int stage) {                 // stage st goes to place `stage`:
+        ba = buffer(a, TA, st);
+        if constexpr (GATED) bu = buffer(up, false, st);
+        bb = buffer(b, TB, st);
+        to = lds0 + stage * C::STAGE;
+        last = st == stages - 1;
     };
+    auto copy = [&](int i) {                               // its copy number i of this wave
+        const bool of_a = i < NA;
+        const int c = wave + WAVES * (of_a ? i : i - NA);
+        if (!of_a && !has_b) return;
+        uint32_t off = of_a ? aoff[i] : boff[i - NA];
+        if (!(of_a ? TA : TB) && last && past(c)) off = kPastEnd;
+        if (!of_a) copy_bounded(to + C::PA * C::RB + c * 1024, off, bb);
+        else if (GATED && c * C::ROWS / F % FA >= FA / 2) copy_bounded(to + c * 1024, off, bu);
+        else copy_bounded(to + c * 1024, off, ba);
+    };
+    constexpr int COPIES = NA + NB1;
     // Waits until all but the newest N stages of this wave's copies have landed, and meets.
     auto landed = [&](auto n) {
         constexpr int N = decltype(n)::value;
         if (NB > 0 || !has_b) core_meet<N * (NA + NB)>();
         else core_meet<N * (NA + 1)>();
-    };
-    // Once a wave has read all that it needs of stage st: wait for stage st + 1, everyone's; the place
-    // of stage st is filled again.
-    auto meet = [&](int st, int stage) {
-        if (st + 1 >= stages) return;
-        if (st + S - 1 < stages) landed(std::integral_constant<int, S - 2>{});
-        else core_meet<0>();
-        if (st + S < stages) fill(st + S, stage);
     };
 #pragma unroll
     for (int j = 0; j < FA; ++j)
@@ -231,48 +222,63 @@ __device__ __forceinline__ void core(char* lds, const Operand& a, const Operand&
 #pragma unroll
             for (int i = 0; i < F * F / 64; ++i) acc[j][m][i] = 0.0f;
     if (stages == 0) return;
-    for (int i = 0; i < S; ++i)
-        if (i < stages) fill(i, i);
-    if (stages >= S) landed(std::integral_constant<int, S - 1>{});
-    else core_meet<0>();
+    for (int i = 0; i < S; ++i) {
+        refill(i, i);
+#pragma unroll
+        for (int c = 0; c < COPIES; ++c) copy(c);
+    }
+    landed(std::integral_constant<int, S - 1>{});
     if (!live) {                                           // it only copies
         for (int st = 0, stage = 0; st < stages; ++st) {
-            meet(st, stage);
+            landed(std::integral_constant<int, S - 2>{});
+            refill(st + S, stage);
+#pragma unroll
+            for (int c = 0; c < COPIES; ++c) copy(c);
             stage = stage + 1 == S ? 0 : stage + 1;
         }
+        core_meet<0>();
         return;
     }
     const Fragments<C, AT, TA, C::PA, FA> fa(wa * F * FA, lane);
     const Fragments<C, AT, TB, C::PB, FB> fb(wb * F * FB, lane);
     typename Fragments<C, AT, TA, C::PA, FA>::Value av[2][FA], bv[2][FB];
-    auto read = [&](int to, const char* st, int kk) {
-#pragma unroll
-        for (int m = 0; m < FB; ++m) bv[to][m] = fb.read(st + C::PA * C::RB, m, kk);
-#pragma unroll
-        for (int j = 0; j < FA; ++j) av[to][j] = fa.read(st, j, kk);
+    auto read = [&](int set, const char* st, int kk, int i) {          // fragment i of those of step kk
+        if (i < FB) bv[set][i] = fb.read(st + C::PA * C::RB, i, kk);
+        else av[set][i - FB] = fa.read(st, i - FB, kk);
     };
-    read(0, lds, 0);
+    constexpr int READS = FA + FB, PRODUCTS = FA * FB;
+#pragma unroll
+    for (int i = 0; i < READS; ++i) read(0, lds, 0, i);
+    static_assert(KK % 2 == 0, "two sets of fragments in turn");
     int stage = 0;
     for (int st = 0; st < stages; ++st) {
         const int next = stage + 1 == S ? 0 : stage + 1;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
-            if (kk + 1 < KK) {
-                read((kk + 1) & 1, lds + stage * C::STAGE, kk + 1);
-            } else {
-                meet(st, stage);
-                if (KK % 2 == 0) read(0, lds + next * C::STAGE, 0);   // behind the last stage: not used
+            // Before a stage's last step a wave has read all that it needs of it: wait for the next
+            // stage, everyone's, and fill this one's place again.  Between the products, in this order,
+            // the reads for the next step and the copies: the compiler's own order puts them first.
+            const bool turn = kk + 1 == KK;
+            if (turn) {
+                landed(std::integral_constant<int, S - 2>{});
+                refill(st + S, stage);
             }
-            __builtin_amdgcn_sched_barrier(0);
+            const char* from = lds + (turn ? next : stage) * C::STAGE;
 #pragma unroll
-            for (int j = 0; j < FA; ++j)
+            for (int i = 0; i < PRODUCTS; ++i) {
+                const int j = i / FB, m = i % FB;
+                acc[j][m] = multiply<F>(av[kk & 1][j], bv[kk & 1][m], acc[j][m]);
 #pragma unroll
-                for (int m = 0; m < FB; ++m) acc[j][m] = multiply<F>(av[kk & 1][j], bv[kk & 1][m], acc[j][m]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int k = i * READS / PRODUCTS; k < (i + 1) * READS / PRODUCTS; ++k) read((kk + 1) & 1, from, turn ? 0 : kk + 1, k);
+                if (turn)
+#pragma unroll
+                    for (int k = i * COPIES / PRODUCTS; k < (i + 1) * COPIES / PRODUCTS; ++k) copy(k);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
-        static_assert(KK % 2 == 0, "two sets of fragments in turn");
         stage = next;
     }
+    core_meet<0>();                                        // the copies of zeros, too, before the ring is used again
 }
 
 // Bytes that a wave's sums take on their way out.
@@ -281,8 +287,7 @@ constexpr int kOutPitch = C::FA * C::F + 4;               // floats of a row: ro
 template <class C>
 constexpr int kOutBytes = C::WAVES * C::F * kOutPitch<C> * 4;
 template <class C>
-constexpr int kCoreLds = C::LDS > kOutBytes<C> ? C::LDS : kOutBytes<C>;
-static_assert(kOutBytes<CoreTile<256, 256, 2, 4, 32, 64, 4>> <= 160 * 1024, "");
+constexpr int kCoreLds = C::LDS > kOutBytes<C> ? C::LDS : kOutBytes<C>;   // of a workgroup
 
 // The sums leave through LDS, F rows of a wave at a time, so that a lane has eight consecutive columns
 // of a row and the lanes side by side the next ones: f(row, column, v, up) for all rows below `rows`,

@@ -65,31 +65,51 @@ struct CoreTile {
     static_assert(S >= 2 && LDS <= 160 * 1024 && (RB == 128 || (RB == 64 && F == 32)), "");
 };
 
+// f of the tile of a product in the activation format, by the rows that a group has on average and by
+// the workgroups that a tile gives (256 CUs), N the columns of its output.  The largest one wins whose
+// tiles the groups fill and which still gives nearly every CU a workgroup.  Measured (us, bf16; both
+// sides of each border; 64 groups, 2048 x 2048 where nothing else is said):
+//   256 x 256 / 256 x 128   512 rows a group, 4096 x 4096: 1214 / 1280;  256 rows: 241 / 220;
+//                           one group, 4096 x 4096: 4096 rows 113 / 150, 2048 rows (128 tiles) 93 / 65
+//   256 x 128 / 128 x 64    256 rows a group: 220 / 262;  128: 169 / 168;  64: 142 / 130;
+//                           one group, 2048 rows (128 tiles): 28.7 / 25.6
+//   128 x 64 / 64 x 32      64 rows a group: 130 / 150;  32: 116 / 111;  16: 125 / 104;
+//                           one group: 1024 rows 16.1 / 21.9, 512 rows (128 tiles) 14.7 / 12.7
+//   64 x 32 / 32 x 32       one group: 4096 x 4096, one row (64 tiles) 15.2 / 12.9;
+//                           333 x 1000, depth 1040 (176 tiles): 7.1 / 8.4
+//   fp32, 128 x 64 / 64 x 32   8 groups of 1024 rows, 4096 x 2048: 1075 / 1173;  of 512, 2048 x 2048: 324 / 318;
+//                           one group, 2048 x 2048: 4096 rows 255 / 287, 1024 rows 79 / 77
+// (fp32's products take sixteen times as long: larger tiles gain nothing over 128 x 64).
 template <class F>
-auto expert_tile(int64_t M, int64_t G, int64_t N, bool offsets, F f) {
+auto expert_tile(bool bf16, int64_t M, int64_t G, int64_t N, bool offsets, F f) {
     const int64_t avg = M / G;
     auto fills = [&](int PA, int PB, int64_t least) { return (N + PA - 1) / PA * most_tiles(M, G, offsets, PB) >= least; };
     constexpr int64_t kMost = 192;
-    if (avg >= 64 && fills(256, 256, kMost)) return f(CoreTile<256, 256, 2, 4, 32, 64, 4>{});
-    if (avg >= 32 && fills(128, 128, kMost)) return f(CoreTile<128, 128, 2, 2, 32, 128, 3>{});
-    if (avg < 16 && fills(128, 16, kMost)) return f(CoreTile<128, 16, 4, 1, 16, 128, 4>{});
-    if (avg >= 16 && fills(64, 64, 128)) return f(CoreTile<64, 64, 1, 2, 32, 128, 4>{});
-    return f(CoreTile<32, 16, 1, 1, 16, 128, 8>{});
+    if (bf16 && avg >= 384 && fills(256, 256, kMost)) return f(CoreTile<256, 256, 2, 4, 32, 128, 2>{});
+    if (bf16 && avg >= 128 && fills(256, 128, kMost)) return f(CoreTile<256, 128, 4, 2, 32, 128, 3>{});
+    if (avg >= (bf16 ? 48 : 768) && fills(128, 64, kMost)) return f(CoreTile<128, 64, 2, 2, 32, 128, 3>{});
+    if (fills(64, 32, 128)) return f(CoreTile<64, 32, 2, 2, 16, 128, 4>{});
+    return f(CoreTile<32, 32, 1, 2, 16, 128, 6>{});
 }
 
-// f of the tile of a matrix' gradient, and the parts that its rows are split into.
+// f of the tile of a matrix' gradient, N x K for each group, and of the parts that a group's rows are
+// split into where the tiles are too few for 256 CUs.  Measured as above:
+//   256 x 256 / 256 x 128   64 groups: 512 rows each 427 / 433, 256 rows 333 / 331, 8 rows 145 / 130;
+//                           one group of 8192 rows, 4096 x 4096: 211 / 241
+//   256 x 128 / 128 x 128   64 groups of 256 rows: 331 / 368;  one of 8192 rows (128 / 256 tiles): 103 / 83
+//   128 x 128 / 128 x 64    one group of 2048 rows, 1024 x 1024 (64 / 128 tiles): 23 / 16
+//   parts 1, 2, 4, 8, 16    one group, 64 x 2048 (16 tiles): 16384 rows 86, -, -, 20.0, 20.9;  4096 rows
+//                           25, 16, 14.2, 14.2, -;  1024 rows 9.8, -, 12.9;  2048 rows, 1024 x 1024: 15.7, 18.3
 template <class F>
 auto matrix_tile(int64_t M, int64_t G, int64_t N, int64_t K, F f) {
-    auto splits = [&](int PA, int PB) {
-        const int64_t tiles = G * ((K + PA - 1) / PA) * ((N + PB - 1) / PB);
-        int64_t n = (384 + tiles - 1) / tiles;
-        const int64_t most = M / G / 512;
-        if (n > most) n = most;
-        return (int)(n > 1 ? n : 1);
-    };
-    if (N >= 192 && K >= 192 && G * ((K + 255) / 256) * ((N + 255) / 256) >= 192)
-        return f(CoreTile<256, 256, 2, 4, 32, 64, 4>{}, 1);
-    return f(CoreTile<128, 64, 2, 2, 32, 128, 4>{}, splits(128, 64));
+    const int64_t avg = M / G;
+    auto tiles = [&](int PA, int PB) { return G * ((K + PA - 1) / PA) * ((N + PB - 1) / PB); };
+    constexpr int64_t kMost = 192;
+    if (avg >= 384 && tiles(256, 256) >= kMost) return f(CoreTile<256, 256, 2, 4, 32, 64, 4>{}, 1);
+    if (tiles(256, 128) >= kMost) return f(CoreTile<256, 128, 4, 2, 32, 64, 3>{}, 1);
+    if (tiles(128, 128) >= kMost) return f(CoreTile<128, 128, 2, 2, 32, 64, 3>{}, 1);
+    const int64_t few = 256 / tiles(128, 64), rows = avg / 2048, n = few < rows ? few : rows;
+    return f(CoreTile<128, 64, 2, 2, 32, 128, 3>{}, (int)(n < 1 ? 1 : n > 16 ? 16 : n));
 }
 
 }  // namespace moe
