@@ -17,7 +17,7 @@ __device__ __forceinline__ float sigmoid(float h) {
 // t that is 0 at t = 0, and P is the polynomial of degree 9 whose largest relative error is least (3.4e-8;
 // fitted to erfcx in fp64 by reweighted least squares).  Off by less than 10 half steps of fp32 and
 // h^2 for the rounding of the exponent.  erfcf took three times as long: 32768 x 4096 gradients
-// in bf16 246 us, GELU us with this (memory: 164).
+// in bf16 246 us, 170 with this (relu 163).
 struct Normal {
     float e, cdf;
     __device__ __forceinline__ explicit Normal(float h) {
