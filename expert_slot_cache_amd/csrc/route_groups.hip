@@ -14,9 +14,10 @@
 //
 // Choices are compared as in 64 bits, for two experts whose scores differ in the tenth digit are
 // no tie.  They are taken in fp32, with a bound of what that may be off, and put in order as in
-// the plain router (sixteen lanes a token up to 512 experts, a wave above that); where two
-// neighbours in that order, or the last group kept and the first left out, lie nearer to each
-// other than the bound, the wave takes that token once more in fp64.  Without a bias the logits
+// the plain router (sixteen lanes a token up to 512 experts, a wave above that).  Where two neighbours
+// among the first K + 1 lie nearer to each other than the bound, the wave takes these K + 1 once more in
+// fp64; where the last group kept and the first left out do, or the last expert chosen and the second
+// one not, all of the token's.  Without a bias the logits
 // themselves are the order, which needs no bound.
 //
 // A group's sum is taken from the largest two of each run of eight (of E / 16 below 128 experts)
@@ -152,6 +153,39 @@ __device__ __forceinline__ void choose_exactly(const void* __restrict__ logits, 
     }
 }
 
+// The K experts of a token among the first K + 1 of its order (K + 1 <= 64), by their choices in fp64, one
+// a lane.  m: the largest logit.
+template <int AT>
+__device__ __forceinline__ void order_exactly(const void* __restrict__ logits, size_t row, const float* __restrict__ bias,
+                                              const RouteGroups& r, float m, uint2* found) {
+    const int lane = threadIdx.x & 63, n = r.K + 1;
+    auto logit = [&](int e) { return fmaxf(load_one<AT>(logits, row + e), -__builtin_inff()); };
+    double sum = 0.0;
+    if (!r.sigmoid) {
+#pragma unroll 4
+        for (int e = lane; e < r.E; e += 64) {
+            const float l = logit(e);
+            sum += exp(l == m ? 0.0 : (double)l - (double)m);
+        }
+        sum = wave_sum64(sum);
+    }
+    const uint2 mine = found[min(lane, n - 1)];
+    const float l = mine.y > 0x7f0000u ? logit((int)mine.x) : 0.0f;      // else none is left
+    const float b = mine.y > 0x7f0000u ? bias[mine.x] : 0.0f;
+    const double t = exp(r.sigmoid ? -(double)l : l == m ? 0.0 : (double)l - (double)m);
+    const double c = (r.sigmoid ? 1.0 : t) / (r.sigmoid ? 1.0 + t : sum) + (double)b;
+    const uint64_t key = mine.y > 0x7f0000u ? key64_of(c == c && l > -__builtin_inff() ? c + 0.0 : -(double)__builtin_inff()) : 0;
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const uint64_t o = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), i) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, i);
+        rank += o > key || (o == key && (uint32_t)__builtin_amdgcn_readlane((int)mine.x, i) < mine.x);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (lane < n) found[rank].x = mine.x;
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Bytes of a wave's choices: fp32 for each of its tokens, or two for each eight, or fp64 for one token
 // (not wanted where the logits are the order and no group is left out).
 template <int L, int V>
@@ -161,7 +195,7 @@ template <int AT, int L, int V>
 __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const void* __restrict__ logits, int64_t stride,
         const float* __restrict__ bias, int T, RouteGroups r, int32_t* __restrict__ ids, float* __restrict__ w) {
     constexpr int PER = 64 / L;                        // tokens of a wave
-    __shared__ uint2 found[kTokensPerBlock][PER][kMaxTopK + 1];   // (id, key) in order
+    __shared__ uint2 found[kTokensPerBlock][PER][kMaxTopK + 2];   // (id, key) in order
     extern __shared__ __align__(16) char shared_c[];   // group_bytes<L, V> a wave
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int sub = lane / L, i = lane % L;            // the wave's token, and the lane in it
@@ -289,7 +323,7 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
     }
     keys.order();
     uint2* f = found[wave][sub];
-    const int rounds = bias ? r.K + 1 : r.K;           // and the first that is not chosen
+    const int rounds = bias ? r.K + 2 : r.K;           // and the first two that are not chosen
     for (int k = 0; k < rounds; ++k) {
         const uint32_t best = keys.best(), top = lanes_max<L>(best);
         bool mine = best == top;
@@ -300,24 +334,31 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
         if (mine) f[k] = make_uint2((uint32_t)(i * V + place), top);
     }
     __builtin_amdgcn_wave_barrier();
+    bool swapped = false;                              // two of the first K + 1 may have to change places
     if (bias) {
+        auto near = [&](const uint2& a, const uint2& b) {
+            if (b.y <= 0x7f0000u) return false;        // none is left
+            const float x = logit_of(a.y), y = logit_of(b.y);
+            return x - y <= off + (fabsf(x) + fabsf(y)) * 0x1p-23f;
+        };
         for (int k = i; k < r.K && here; k += L) {
             const uint2 a = f[k], b = f[k + 1];
-            if (b.y <= 0x7f0000u) continue;            // nothing is left
-            const float x = logit_of(a.y), y = logit_of(b.y);
-            if (!(x - y <= off + (fabsf(x) + fabsf(y)) * 0x1p-23f)) continue;
+            if (!near(a, b)) continue;
             // two chosen ones with the same logit and bias are a tie in fp64 too
-            unsure = unsure || k + 1 == r.K || bias[a.x] != bias[b.x] ||
-                     load_one<AT>(logits, row + a.x) != load_one<AT>(logits, row + b.x);
+            if (k + 1 < r.K && bias[a.x] == bias[b.x] && load_one<AT>(logits, row + a.x) == load_one<AT>(logits, row + b.x)) continue;
+            swapped = true;
+            unsure = unsure || r.K == kMaxTopK || (k + 1 == r.K && near(a, f[k + 2]));
         }
     }
-    uint64_t again = __ballot(unsure && here);
-    while (again) {
-        const int who = __builtin_ctzll(again), token = who / L;
-        again &= L == 64 ? 0 : ~(0xffffull << (16 * token));
-        const int tt = (blockIdx.x * kTokensPerBlock + wave) * PER + token;
-        choose_exactly<AT>(logits, (size_t)tt * (size_t)stride, bias, r,
-                                             reinterpret_cast<uint64_t*>(mine_c), found[wave][token]);
+    uint64_t again = __ballot(unsure && here), swaps = __ballot(swapped && here);
+    while (again | swaps) {
+        const int token = __builtin_ctzll(again | swaps) / L;
+        const uint64_t its = L == 64 ? ~0ull : 0xffffull << (16 * token);
+        const size_t from = (size_t)((blockIdx.x * kTokensPerBlock + wave) * PER + token) * (size_t)stride;
+        if (again & its) choose_exactly<AT>(logits, from, bias, r, reinterpret_cast<uint64_t*>(mine_c), found[wave][token]);
+        else order_exactly<AT>(logits, from, bias, r, __shfl(m, token * L), found[wave][token]);
+        again &= ~its;
+        swaps &= ~its;
     }
     __builtin_amdgcn_wave_barrier();
     float l[kMaxTopK / L], big = low;

@@ -97,6 +97,26 @@ def test_choices_nearer_than_fp32_holds(T, E, K, groups, kept):
         check(dev(near), a_little, K, score="sigmoid", **kw)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,K,groups,kept", [(64, 64, 8, 8, 4), (64, 64, 8, 1, 1), (24, 512, 9, 8, 3), (9, 1024, 64, 1, 1),
+                                              (9, 1024, 63, 4, 3), (33, 20, 19, 1, 1), (33, 20, 20, 1, 1)])
+def test_pairs_of_near_choices(T, E, K, groups, kept, score):
+    """Experts in pairs whose choices differ by the rounding of their fp32 biases, pairs well apart: the
+    order inside a pair, at the border of the chosen ones too, is that of fp64."""
+    rng = np.random.default_rng(E + K)
+    z = np.empty((T, E), np.float32)
+    bias = np.empty(E, np.float32)
+    one = rng.normal(size=E).astype(np.float32)        # the same logits for every token, in another order of pairs
+    s = oe.scores(one.astype(np.float64), score)
+    target = np.repeat(rng.permutation(E // 2 + E % 2) * 0.02, 2)[:E]
+    bias[:] = (target - s).astype(np.float32)
+    z[:] = one
+    turned = rng.random(T) < 0.5                       # softmax: a shift of all logits changes no score
+    z[turned] += np.float32(1.0) if score == "softmax" else np.float32(0.0)
+    for top in (1, 2):
+        check(dev(z), bias, K, score=score, renorm=True, n_groups=groups, kept=kept, group_top=top)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 def test_scores_far_below_fp32(renorm):
     """Sigmoids of -60 to -200: renormalised weights keep their ratios."""
