@@ -132,7 +132,7 @@ hipError_t launch_activation_backward(int atype, int out_atype, const Activation
     const int rows = act_rows(a.M, a.G, a.N);
     const int nblocks = ((a.act == ACT_SWIGLU ? a.N / 2 : a.N) + kActCols - 1) / kActCols;
     const int64_t grid = nblocks * most_tiles(a.M, a.G, a.offsets, rows);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!launchable(grid, 4)) return hipErrorInvalidValue;
     auto run = [&](auto at, auto ot, auto act) {
         constexpr int AT = decltype(at)::value, OT = decltype(ot)::value, ACT = decltype(act)::value;
         if (rows == 16)

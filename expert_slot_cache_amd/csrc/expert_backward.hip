@@ -98,7 +98,7 @@ template <class C, int AT>
 hipError_t rows(const ExpertGradArgs& p, hipStream_t s) {
     const int nblocks = (p.K + C::PA - 1) / C::PA;
     const int64_t grid = (nblocks * most_tiles(p.M, p.G, p.offsets, C::PB) + 7) / 8 * 8;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (!launchable(grid, C::WAVES)) return hipErrorInvalidValue;
     hipLaunchKernelGGL((k_expert_rows<C, AT>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, p, nblocks);
     return hipGetLastError();
 }
@@ -109,7 +109,7 @@ hipError_t matrices(const ExpertGradArgs& p, int dw_at, hipStream_t s) {
         typedef decltype(tile) C;
         const int kblocks = (p.K + C::PA - 1) / C::PA, tiles = kblocks * ((p.N + C::PB - 1) / C::PB);
         const int64_t grid = (int64_t)tiles * splits * p.G;
-        if (grid > 0x7fffffff) return hipErrorInvalidValue;
+        if (!launchable(grid, C::WAVES)) return hipErrorInvalidValue;
         hipLaunchKernelGGL((k_expert_matrices<C, AT>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, p, dw_at, kblocks, tiles,
                            splits);
         if (splits > 1) {

@@ -49,7 +49,10 @@ auto product_tile(int64_t M, int64_t G, int64_t N, bool offsets, F f) {
 }
 
 // ---- products in the activation format ----
-//
+
+// A launch has fewer than 2^32 lanes.
+inline bool launchable(int64_t workgroups, int waves) { return workgroups * 64 * waves < (int64_t)1 << 32; }
+
 // A workgroup of WA x WB waves computes PA columns x PB rows of the output, in fragments of F x F
 // (the columns are the instruction's A operand, so that four accumulators of a lane are consecutive
 // columns).  A stage of the ring holds RB bytes of the summed dimension of each of them; S stages.

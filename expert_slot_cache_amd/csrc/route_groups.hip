@@ -303,8 +303,10 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
                     mine = false;
                 }
         }
-        // infinite scores that are alike are so in fp64 too (their difference is NaN)
-        if (bias || r.group_top > 1) unsure = least - most <= 2.0f * off + (fabsf(least) + fabsf(most)) * 0x1p-22f;
+        // a sum of two that runs over fp32 has no difference either (NaN); a group of masked experts is left
+        // out, or kept in its order, as it is
+        if (bias || r.group_top > 1)
+            unsure = most > low && !(least - most > 2.0f * off + (fabsf(least) + fabsf(most)) * 0x1p-22f);
         lo = lanes_or<L>(lo);
         hi = lanes_or<L>(hi);
         kept = (uint64_t)hi << 32 | lo;

@@ -18,4 +18,8 @@ leg do.  It shares no code with the HIP library.
   gathered gate weights ("Running 125B MoE on Two 32 GB Cards", section 4.2).
 * ``oracle.moe`` -- the slot-indexed MoE layer in float64: dequantisation of the
   expert bytes, w13 projection, SwiGLU, w2 projection and the top-k weighted sum.
+* ``oracle.rows`` -- the router's top-k, tokens sorted by expert and back, e4m3 rows and
+  products, with gradients.
+* ``oracle.experts`` -- the router with biased choices among groups, and the products of
+  sorted rows with their experts' matrices, their epilogue and their gradients.
 """

@@ -117,6 +117,15 @@ def test_pairs_of_near_choices(T, E, K, groups, kept, score):
         check(dev(z), bias, K, score=score, renorm=True, n_groups=groups, kept=kept, group_top=top)
 
 
+def test_group_sums_that_run_over_fp32():
+    """Biases near fp32's largest value: two of them have no sum in fp32, and differ in fp64."""
+    rng = np.random.default_rng(4)
+    bias = np.full(32, 2.0e38, np.float32)
+    bias += (rng.integers(0, 1000, 32) * 2.0 ** 110).astype(np.float32)
+    assert np.isfinite(bias).all() and np.isinf(bias[0] + bias[1])
+    check(dev(rng.normal(size=(9, 32)).astype(np.float32)), bias, 3, score="sigmoid", renorm=False, n_groups=8, kept=3, group_top=2)
+
+
 @pytest.mark.parametrize("renorm", [False, True])
 def test_scores_far_below_fp32(renorm):
     """Sigmoids of -60 to -200: renormalised weights keep their ratios."""
