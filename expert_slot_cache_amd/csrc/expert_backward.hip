@@ -130,7 +130,7 @@ size_t expert_backward_workspace(int atype, int M, int G, int N, int K) {
 
 hipError_t launch_expert_backward(int atype, int dw_atype, const ExpertGradArgs& p, hipStream_t s) {
     if (p.dx && p.M > 0) {
-        const hipError_t e = expert_tile(atype == A_BF16, p.M, p.G, p.K, p.offsets, [&](auto tile) {
+        const hipError_t e = expert_tile<false>(atype == A_BF16, p.M, p.G, p.K, p.offsets, [&](auto tile) {
             typedef decltype(tile) C;
             return atype == A_F32 ? rows<C, A_F32>(p, s) : rows<C, A_BF16>(p, s);
         });

@@ -12,7 +12,8 @@ int main() {
     while (std::scanf(" %c %d %lld %lld %lld %lld %d", &rule, &bf16, &M, &G, &N, &K, &offsets) == 7) {
         auto print = [](auto t, int parts) { return std::printf("%d %d %d %d %d\n", t.PA, t.PB, t.RB, t.S, parts); };
         if (rule == 'm') moe::matrix_tile(M, G, N, K, print);
-        else moe::expert_tile(bf16 != 0, M, G, N, offsets != 0, [&](auto t) { return print(t, 1); });
+        else if (rule == 's') moe::expert_tile<true>(bf16 != 0, M, G, N, offsets != 0, [&](auto t) { return print(t, 1); });
+        else moe::expert_tile<false>(bf16 != 0, M, G, N, offsets != 0, [&](auto t) { return print(t, 1); });
     }
     return 0;
 }

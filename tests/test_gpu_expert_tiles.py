@@ -13,13 +13,15 @@ BF16 = {
     (256, 256): [(3000, 2, 4096, 256), (3001, 2, 4112, 328)],
     (256, 128): [(1600, 8, 2560, 384), (1601, 8, 2576, 360)],
     (128, 64): [(1000, 16, 896, 384), (1001, 16, 912, 328)],
+    (64, 64): [(700, 16, 512, 384), (701, 16, 528, 392)],
     (64, 32): [(60, 30, 320, 448), (61, 30, 336, 520), (333, 1, 1000, 1040)],
     (32, 32): [(20, 3, 64, 512), (21, 3, 80, 600), (1, 1, 2048, 1024)],
 }
 F32 = {
     (128, 64): [(1700, 2, 896, 192), (1701, 2, 912, 212)],
-    (64, 32): [(60, 30, 320, 224), (333, 1, 1000, 260), (3000, 8, 512, 196)],
-    (32, 32): [(20, 3, 64, 256), (21, 3, 80, 292)],
+    (64, 64): [(700, 16, 512, 192), (701, 16, 528, 196), (3000, 8, 512, 196)],
+    (64, 32): [(120, 60, 320, 224), (121, 60, 336, 228)],
+    (32, 32): [(20, 3, 64, 256), (21, 3, 80, 292), (333, 1, 1000, 260)],
 }
 # (columns, rows of a tile, parts): (rows, groups, columns, depth) of a product whose matrix' gradient it is
 MATRICES = {
