@@ -20,10 +20,11 @@
 // one not, all of the token's.  Without a bias the logits
 // themselves are the order, which needs no bound.
 //
-// A group's sum is taken from the largest two of each run of eight (of E / 16 below 128 experts)
+// A group's sum is taken from the largest two of each run of eight (of fewer below 65 experts)
 // where every such run lies in one group, else from its experts one by one.  16384 tokens of 512
 // experts, top-10 in fp32, sigmoid, take 17 us without bias and groups, 21 with the 4 best of 8 groups,
-// 36 with a bias: about one token in a thousand is taken again, and the call waits for the last.
+// 29 with a bias: about one token in a thousand is taken again, and the call waits for the last (36 us
+// where each of them was with all of its experts).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -64,9 +65,8 @@ __device__ __forceinline__ double wave_sum64(double v) {
 }
 
 // A token by a whole wave in fp64: its K experts into `found`, in order.  cs: 8 E bytes in LDS, the
-// logits and biases, then the choices, then their order.  Few tokens come here, but the call waits for
-// them, mostly for their instructions (nothing has fetched these before: unrolled loops took twice as
-// long), so only loads are requested several at a time.
+// logits and biases, then the choices, then their order.  Few tokens come here, and every token's wave
+// has the registers and the code that this takes: loops over LDS, loads requested four at a time.
 template <int AT>
 __device__ __forceinline__ void choose_exactly(const void* __restrict__ logits, size_t row, const float* __restrict__ bias,
                                                const RouteGroups& r, uint64_t* cs, uint2* found) {

@@ -194,6 +194,10 @@ def test_activation_backward(M, G, N, act, kind, out):
     binding.activation_backward(d_out, pre, alone, act=act, offsets=off)
     binding.activation_backward(d_out, pre, None, d_bias=alone_b, act=act, offsets=off)
     assert torch.equal(alone, dp.t) and torch.equal(alone_b, db.t)
+    if act == "none" and kind == out:
+        same = d_out.clone()
+        binding.activation_backward(same, None, same, offsets=off)
+        assert torch.equal(same, d_out)
     if act != "none":
         binding.activation_backward(d_out, pre, pre, act=act, offsets=off)
         rows = torch.from_numpy(~out_of).to(DEV)
