@@ -76,16 +76,18 @@ struct CoreTile {
 //                           one group, 4096 x 4096: 4096 rows 113 / 150, 2048 rows (128 tiles) 93 / 65
 //   256 x 128 / 128 x 64    256 rows a group: 220 / 262;  128: 169 / 168;  64: 142 / 130;
 //                           one group, 2048 rows (128 tiles): 28.7 / 25.6
-//   128 x 64 / 64 x 64      64 rows a group: 130 / 151;  32: 116 / 110;
-//                           one group: 1024 rows 16.1 / 16.3, 512 rows (128 tiles) 14.7 / 12.6
-//   64 x 64 / 64 x 32       32 rows a group: 110 / 112, back to the rows 107 / 118;  16: 133 / 104;
-//                           one group: 512 rows 12.6 / 13.5;  333 x 1000, depth 1040 (96 tiles): 8.2 / 7.0
+//   128 x 64 / 64 x 64      64 rows a group: 129 / 136;  32: 120 / 117;
+//                           one group: 1024 rows 17.0 / 18.1, 512 rows (128 tiles) 15.6 / 12.9
+//   64 x 64 / 64 x 32       32 rows a group: 117 / 112, back to the rows 113 / 120;  16: 108 / 96;
+//                           one group: 512 rows 12.9 / 14.1;  333 x 1000, depth 1040 (96 tiles): 8.2 / 7.0
 //   64 x 32 / 32 x 32       one group: 4096 x 4096, one row (64 tiles) 17.4 / 11.2;  64 rows (64 tiles) 8.7 / 7.8;
 //                           333 x 1000 (176 tiles): 7.0 / 8.0
-//   fp32, 128 x 64 / 64 x 64   8 groups of 1024 rows, 4096 x 2048: 1075 / 1215;  of 512, 2048 x 2048: 324 / 297
+//   fp32, 128 x 64 / 64 x 64   8 groups of 1024 rows, 4096 x 2048: 1188 / 1074;  of 512, 2048 x 2048: 321 / 290;
+//                           with the 64 x 64 of SwiGLU: 1075 / 1215 and 324 / 357
+//   fp32, 64 x 64 / 64 x 32    8 groups of 512 rows: 290 / 298;  64 of 16 rows, 1024 x 1024: 91 / 64
 //   fp32, 64 x 32 / 32 x 32    333 x 1000 (176 tiles): 15.1 / 13.8;  64 rows (64 tiles): 24.3 / 15.0;
 //                           64 groups of 16 rows, 1024 x 1024: 64 / 58;  one row each: 35.3 / 35.2
-// (fp32's products take sixteen times as long: larger tiles gain nothing over 128 x 64).  SwiGLU's small
+// (fp32's products take sixteen times as long: larger tiles gain nothing).  SwiGLU's small
 // tiles have two waves instead of four: a wave's fragments are gate and up.
 template <bool SWIGLU, class F>
 auto expert_tile(bool bf16, int64_t M, int64_t G, int64_t N, bool offsets, F f) {
@@ -94,7 +96,7 @@ auto expert_tile(bool bf16, int64_t M, int64_t G, int64_t N, bool offsets, F f) 
     constexpr int64_t kMost = 192;
     if (bf16 && avg >= 384 && fills(256, 256, kMost)) return f(CoreTile<256, 256, 2, 4, 32, 128, 2>{});
     if (bf16 && avg >= 128 && fills(256, 128, kMost)) return f(CoreTile<256, 128, 4, 2, 32, 128, 3>{});
-    if (avg >= (bf16 ? 48 : 768) && fills(128, 64, kMost)) return f(CoreTile<128, 64, 2, 2, 32, 128, 3>{});
+    if ((bf16 ? avg >= 48 : SWIGLU && avg >= 768) && fills(128, 64, kMost)) return f(CoreTile<128, 64, 2, 2, 32, 128, 3>{});
     if (avg >= 32 && fills(64, 64, kMost)) return f(CoreTile<64, 64, SWIGLU ? 1 : 2, 2, 32, 128, SWIGLU ? 4 : 3>{});
     if (fills(64, 32, bf16 ? 128 : 256)) return f(CoreTile<64, 32, 2, 2, 16, 128, 4>{});
     return f(CoreTile<32, 32, SWIGLU ? 1 : 2, 2, 16, 128, 6>{});

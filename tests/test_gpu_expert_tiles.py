@@ -18,10 +18,12 @@ BF16 = {
     (32, 32): [(20, 3, 64, 512), (21, 3, 80, 600), (1, 1, 2048, 1024)],
 }
 F32 = {
-    (128, 64): [(1700, 2, 896, 192), (1701, 2, 912, 212)],
     (64, 64): [(700, 16, 512, 192), (701, 16, 528, 196), (3000, 8, 512, 196)],
     (64, 32): [(120, 60, 320, 224), (121, 60, 336, 228)],
     (32, 32): [(20, 3, 64, 256), (21, 3, 80, 292), (333, 1, 1000, 260)],
+}
+F32_SWIGLU = {                                        # and this one, which SwiGLU alone takes in fp32
+    (128, 64): [(1700, 2, 896, 192), (1701, 2, 912, 212)],
 }
 # (columns, rows of a tile, parts): (rows, groups, columns, depth) of a product whose matrix' gradient it is
 MATRICES = {
@@ -41,7 +43,7 @@ def test_products_in_bf16(M, G, N, K):
         product_case(M, G, N, K, "bf16", "f32", "swiglu", True, False, True, holes=M % 2 == 0, seed=5)
 
 
-@pytest.mark.parametrize("M,G,N,K", [c for cases in F32.values() for c in cases])
+@pytest.mark.parametrize("M,G,N,K", [c for table in (F32, F32_SWIGLU) for cases in table.values() for c in cases])
 def test_products_in_fp32(M, G, N, K):
     product_case(M, G, N, K, "f32", "f32", "none", False, True, False, holes=M % 2 == 1)
     if N % 8 == 0:
