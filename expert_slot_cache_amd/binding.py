@@ -728,13 +728,12 @@ def activation_backward(d_out, pre, d_pre=None, *, d_bias=None, act: str = "none
     ot = _atype(torch, "d_out", d_out)
     M, cols = _array("d_out", d_out, d_out.dtype, dev)
     N = 2 * cols if act == "swiglu" else cols
-    kind = pre.dtype if pre is not None else d_pre.dtype if d_pre is not None else d_out.dtype
+    like = pre if pre is not None else d_pre if d_pre is not None else d_out
+    at, kind = _atype(torch, "pre" if like is pre else "d_pre", like), like.dtype
     if act != "none" or pre is not None:
         _check_tensor("pre", pre, kind, (M, N), dev)
-    at = A_BF16 if kind is torch.bfloat16 else A_F32
     _same_or_f32(torch, "d_out", d_out, kind)
     if d_pre is not None:
-        _atype(torch, "d_pre", d_pre)
         _check_tensor("d_pre", d_pre, kind, (M, N), dev)
     G = 1
     if offsets is not None:
