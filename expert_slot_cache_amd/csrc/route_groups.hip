@@ -274,8 +274,10 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
                 one = fmaxf(one, v.x);
                 o = o + 1 == parts ? 0 : o + 1;
             }
-            if (r.group_top > 1 && !bias) one = (one > low ? score_of(one) : low) + (two > low ? score_of(two) : 0.0f);
-            else if (r.group_top > 1 && two > low) one += two;
+            if (r.group_top > 1) {                         // half the sum, so that no two choices run over fp32
+                if (!bias) one = one > low ? score_of(one) : low, two = two > low ? score_of(two) : low;
+                one = 0.5f * one + (two > low ? 0.5f * two : 0.0f);
+            }
             gk[a] = key_of(one);
         }
         // the kept groups, one after another, and the first that is not
@@ -303,10 +305,10 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
                     mine = false;
                 }
         }
-        // a sum of two that runs over fp32 has no difference either (NaN); a group of masked experts is left
-        // out, or kept in its order, as it is
+        // Halves of two choices, or one of them, each off by off / 2.  A group of masked experts is left out,
+        // or kept in its order, as it is.
         if (bias || r.group_top > 1)
-            unsure = most > low && !(least - most > 2.0f * off + (fabsf(least) + fabsf(most)) * 0x1p-22f);
+            unsure = most > low && !(least - most > off + (fabsf(least) + fabsf(most)) * 0x1p-22f);
         lo = lanes_or<L>(lo);
         hi = lanes_or<L>(hi);
         kept = (uint64_t)hi << 32 | lo;
