@@ -31,6 +31,7 @@
 
 #include "ops.hpp"
 #include "route_dev.hpp"
+#include "route_doubt.hpp"
 
 namespace moe {
 namespace {
@@ -257,10 +258,13 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
             for (int j = 0; j < V; ++j) to[j] = c[j];
         }
         __builtin_amdgcn_wave_barrier();                   // LDS operations of one wave complete in order
-        uint32_t gk[kMaxGroups / L];
+        constexpr int GROUPS = kMaxGroups / L;             // of a lane
+        uint32_t gk[GROUPS];
+        GroupSum sums[GROUPS];
 #pragma unroll
-        for (int a = 0; a < kMaxGroups / L; ++a) {
+        for (int a = 0; a < GROUPS; ++a) {
             gk[a] = 0;
+            sums[a] = {low, 0.0f};
             const int q = i * each + a;
             if (a >= each || q >= r.n_groups) continue;
             float one = low, two = low;
@@ -274,29 +278,26 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
                 one = fmaxf(one, v.x);
                 o = o + 1 == parts ? 0 : o + 1;
             }
-            if (r.group_top > 1) {                         // half the sum, so that no two choices run over fp32
-                if (!bias) one = one > low ? score_of(one) : low, two = two > low ? score_of(two) : low;
-                one = 0.5f * one + (two > low ? 0.5f * two : 0.0f);
+            if (r.group_top > 1 && !bias) {                // these are logits
+                one = one > low ? score_of(one) : low;
+                two = two > low ? score_of(two) : low;
             }
-            gk[a] = key_of(one);
+            sums[a] = group_sum(one, two, r.group_top > 1, off);
+            gk[a] = key_of(sums[a].value);
         }
-        // the kept groups, one after another, and the first that is not
+        // the kept groups, one after another
         uint32_t lo = 0, hi = 0;
-        float least = 0.0f, most = 0.0f;
-        for (int k = 0; k <= r.kept; ++k) {
+        for (int k = 0; k < r.kept; ++k) {
             uint32_t best = 0;
 #pragma unroll
-            for (int a = 0; a < kMaxGroups / L; ++a) best = max(best, gk[a]);
+            for (int a = 0; a < GROUPS; ++a) best = max(best, gk[a]);
             const uint32_t top = lanes_max<L>(best);
-            least = most;
-            most = logit_of(top);
-            if (k == r.kept) break;
             const uint64_t holds = __ballot(best == top);
             bool mine = best == top;
             if constexpr (L == 64) mine = lane == __builtin_ctzll(holds);
             else mine = mine && (holds & below) == 0;
 #pragma unroll
-            for (int a = 0; a < kMaxGroups / L; ++a)
+            for (int a = 0; a < GROUPS; ++a)
                 if (mine && gk[a] == top) {
                     const int q = i * each + a;
                     if (q < 32) lo |= 1u << q;
@@ -305,10 +306,22 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
                     mine = false;
                 }
         }
-        // Halves of two choices, or one of them, each off by off / 2.  A group of masked experts is left out,
-        // or kept in its order, as it is.
-        if (bias || r.group_top > 1)
-            unsure = most > low && !(least - most > off + (fabsf(least) + fabsf(most)) * 0x1p-22f);
+        // Is the least that any kept one may be above the most that any other may?  (Of largest logits
+        // nothing is off.)  Where all that are left out are groups of masked experts, those kept are the first.
+        if (bias || r.group_top > 1) {
+            float least = __builtin_inff(), most = low;
+#pragma unroll
+            for (int a = 0; a < GROUPS; ++a) {
+                const int q = i * each + a;
+                const bool is_kept = ((q < 32 ? lo >> q : hi >> (q - 32)) & 1) != 0;
+                if (a >= each || q >= r.n_groups) continue;
+                if (is_kept) least = fminf(least, sums[a].value - sums[a].off);
+                else most = fmaxf(most, sums[a].value + sums[a].off);
+            }
+            least = -logit_of(lanes_max<L>(key_of(-least)));
+            most = logit_of(lanes_max<L>(key_of(most)));
+            unsure = most > low && !(least > most);
+        }
         lo = lanes_or<L>(lo);
         hi = lanes_or<L>(hi);
         kept = (uint64_t)hi << 32 | lo;
