@@ -21,4 +21,12 @@ constexpr GroupSum group_sum(float one, float two, bool pairs, float off) {
     return {0.5f * one + second, finite ? 0.5f * off + (0.5f * magnitude(one) + magnitude(second)) * 0x1p-22f : 0.0f};
 }
 
+// May the choice y, no larger than x, lie above it in fp64?  Each is off by off / 2 and by half a step.
+// Next to an infinite choice the order is in no doubt: masked experts (-inf) are behind all others, and
+// among themselves in id order.
+constexpr bool near_choices(float x, float y, float off) {
+    const float gap = x - y;                           // of equal infinities NaN
+    return gap < __builtin_inff() && gap <= off + (magnitude(x) + magnitude(y)) * 0x1p-23f;
+}
+
 }  // namespace moe

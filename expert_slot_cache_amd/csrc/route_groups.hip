@@ -354,9 +354,7 @@ __global__ __launch_bounds__(64 * kTokensPerBlock) void k_route_groups(const voi
     bool swapped = false;                              // two of the first K + 1 may have to change places
     if (bias) {
         auto near = [&](const uint2& a, const uint2& b) {
-            if (b.y <= 0x7f0000u) return false;        // none is left
-            const float x = logit_of(a.y), y = logit_of(b.y);
-            return x - y <= off + (fabsf(x) + fabsf(y)) * 0x1p-23f;
+            return b.y > 0x7f0000u && near_choices(logit_of(a.y), logit_of(b.y), off);   // else none is left
         };
         for (int k = i; k < r.K && here; k += L) {
             const uint2 a = f[k], b = f[k + 1];

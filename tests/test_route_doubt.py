@@ -62,3 +62,12 @@ def test_sums_of_infinite_and_lowest_choices(driver):
                   (3e38, 3e38, 1, 1e-6), (1.0, LOWEST, 1, 1e-6), (0.5, -INF, 1, 0.0), (INF, -1.0, 0, 1e-6), (-INF, -INF, 0, 1e-6)])
     assert [v for v, _ in got] == [INF, INF, -INF, LOWEST, f32(3e38), LOWEST / 2, 0.25, INF, -INF]
     assert [bound for _, bound in got[:3]] == [0, 0, 0] and all(np.isfinite(bound) for _, bound in got)
+
+
+def test_choices_next_to_masked_ones_are_in_no_doubt(driver):
+    off = 2.0 ** -21
+    near = lambda *pairs: [v for v, in driver([(repr(x), repr(y), 2, repr(off)) for x, y in pairs])]      # noqa: E731
+    assert near((0.5, -INF), (-1e5, -INF), (LOWEST, -INF), (-INF, -INF), (INF, 1.0), (INF, LOWEST), (INF, -INF), (INF, INF),
+                (0.5, LOWEST), (2e38, -2e38)) == [0] * 10
+    assert near((0.5, 0.5), (0.0, -0.0), (0.5, 0.5 - off), (0.5 + 2 * off, 0.5), (1e5, f32(1e5 - 0.01)), (1e5, f32(1e5 - 0.04)),
+                (LOWEST, LOWEST)) == [1, 1, 1, 0, 1, 0, 1]
