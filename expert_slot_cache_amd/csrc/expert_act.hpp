@@ -38,14 +38,15 @@ struct Normal {
     }
 };
 
+// A NaN stays one through every activation and slope.
 __device__ __forceinline__ float activate(int act, float h) {
-    if (act == ACT_RELU) return h > 0.0f ? h : 0.0f;
+    if (act == ACT_RELU) return h <= 0.0f ? 0.0f : h;
     if (act == ACT_GELU) return h * Normal(h).cdf;
     if (act == ACT_SILU) return h * sigmoid(h);
     return h;
 }
 __device__ __forceinline__ float slope(int act, float h) {
-    if (act == ACT_RELU) return h > 0.0f ? 1.0f : 0.0f;
+    if (act == ACT_RELU) return h > 0.0f ? 1.0f : h <= 0.0f ? 0.0f : h;
     if (act == ACT_GELU) {
         const Normal v(h);
         return fmaf(h * 0.39894228f, v.e, v.cdf);

@@ -607,6 +607,7 @@ moe_status_t moe_scaled_product(const void* x_dev, const float* x_scales_dev, co
  *  act           MOE_ACT_NONE; _RELU; _GELU, h times the normal distribution function of h; _SILU,
  *                h / (1 + exp(-h)); _SWIGLU (n_cols a multiple of 16, fp32: 8): columns [0, n_cols/2)
  *                are the gate, the rest the up projection: silu(gate) * up, n_cols/2 outputs a row.
+ *                A NaN in h leaves as NaN, an infinity as the formula has it (0 inf is NaN).
  *  out_dev       [n_rows][n_cols (SwiGLU: n_cols/2)] in out_atype, fp32 or the activation format;
  *  resid_dev     the same, or NULL: none.  It may be out_dev itself.
  *  pre_dev       [n_rows][n_cols] in the activation format, written: h (for the gradient); or NULL.
@@ -631,8 +632,9 @@ moe_status_t moe_expert_product(int32_t atype, const void* x_dev, const void* w_
  *                MOE_ACT_NONE in the same format d_out_dev.
  *  workspace_dev moe_activation_backward_workspace_bytes(n_rows, n_groups, n_cols) bytes on 16
  *                where d_bias_dev is given, used by this call only.
- * A group without rows has a d_bias of 0 (n_rows = 0 as well).  Sizes, offsets, alignment and the
- * rows outside every group as in moe_expert_product.  Errors: EINVAL, EHIP. */
+ * act' at NaN is NaN, relu's at 0 is 0.  A group without rows has a d_bias of 0 (n_rows = 0 as well).
+ * Sizes, offsets, alignment and the rows outside every group as in moe_expert_product.
+ * Errors: EINVAL, EHIP. */
 moe_status_t moe_activation_backward(int32_t atype, const void* d_out_dev, int32_t out_atype, const void* pre_dev,
                                      const int32_t* offsets_dev, int32_t n_rows, int32_t n_groups, int32_t n_cols,
                                      int32_t act, void* d_pre_dev, float* d_bias_dev, void* workspace_dev,

@@ -97,7 +97,7 @@ def sigmoid(h: np.ndarray) -> np.ndarray:
 
 def activate(h: np.ndarray, act: str) -> np.ndarray:
     if act == "relu":
-        return np.where(h > 0, h, 0.0)
+        return np.where(h <= 0, 0.0, h)                # NaN stays NaN
     if act == "gelu":
         return h * normal_cdf(h)
     if act == "silu":
@@ -110,7 +110,7 @@ def activate(h: np.ndarray, act: str) -> np.ndarray:
 
 def slope(h: np.ndarray, act: str) -> np.ndarray:
     if act == "relu":
-        return (h > 0).astype(np.float64)
+        return np.where(np.isnan(h), h, h > 0)
     if act == "gelu":
         return normal_cdf(h) + h * np.exp(-0.5 * h * h) / math.sqrt(2.0 * math.pi)
     if act == "silu":
