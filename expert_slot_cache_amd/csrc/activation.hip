@@ -7,8 +7,8 @@
 // so that a thread has eight rows to itself, whose loads are requested four at a time, and a small
 // call still gives many CUs work: 333 x 1000 in fp32, GELU, takes 12.0 us (one thread to a
 // column's 64 rows: 31.7).  32768 rows, SwiGLU of 4096 columns, bf16, with the bias' gradient (671 MB): 140 us.  The
-// bias' sums are fp32: a thread's rows, then the eight threads of a column, then the tiles of a group in
-// a second launch, each in a fixed order.
+// bias' sums are fp32 in a tile (a thread's eight rows, then the eight threads of a column) and fp64 over the
+// tiles of a group, in a second launch, each in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include "expert_act.hpp"
@@ -100,9 +100,11 @@ __global__ __launch_bounds__(256) void k_activation_backward(ActivationArgs p, i
     }
 }
 
-// The sums of a group's tiles: 32 columns by eight slices of the tiles.
+// The sums of a group's tiles: 32 columns by eight slices of the tiles.  In fp64, for a slice of 2^24 rows is a
+// chain of 32768 additions.  Its loads bound it, sixteen at a time: both launches of 2^22 rows of 16 columns
+// in fp32 take 577 us (eight at a time, fp64: 729, fp32: 703).
 __global__ __launch_bounds__(256) void k_bias_sums(ActivationArgs p, int rows) {
-    __shared__ float sums[8][32];
+    __shared__ double sums[8][32];
     const int g = blockIdx.y, lane = threadIdx.x & 31, slice = threadIdx.x >> 5, n = blockIdx.x * 32 + lane;
     int lo = 0, hi = p.M;
     if (p.offsets) {
@@ -110,10 +112,10 @@ __global__ __launch_bounds__(256) void k_bias_sums(ActivationArgs p, int rows) {
         hi = min(max(p.offsets[g + 1], lo), p.M);
     }
     const int tiles = (hi - lo + rows - 1) / rows;
-    float v = 0.0f;
+    double v = 0.0;
     if (n < p.N) {
         const float* from = p.partial + place(lo, g, rows) * p.N + n;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = slice; i < tiles; i += 8) v += from[(size_t)i * p.N];
     }
     sums[slice][lane] = v;
@@ -121,7 +123,7 @@ __global__ __launch_bounds__(256) void k_bias_sums(ActivationArgs p, int rows) {
     if (slice || n >= p.N) return;
 #pragma unroll
     for (int s = 1; s < 8; ++s) v += sums[s][lane];
-    p.dbias[(size_t)g * p.N + n] = v;
+    p.dbias[(size_t)g * p.N + n] = (float)v;
 }
 
 }  // namespace
