@@ -133,8 +133,7 @@ size_t activation_workspace(int M, int G, int N) { return (size_t)(M / act_rows(
 hipError_t launch_activation_backward(int atype, int out_atype, const ActivationArgs& a, hipStream_t s) {
     const int rows = act_rows(a.M, a.G, a.N);
     const int nblocks = ((a.act == ACT_SWIGLU ? a.N / 2 : a.N) + kActCols - 1) / kActCols;
-    const int64_t grid = nblocks * most_tiles(a.M, a.G, a.offsets, rows);
-    if (!launchable(grid, 4)) return hipErrorInvalidValue;
+    const int64_t grid = nblocks * most_tiles(a.M, a.G, a.offsets, rows);   // 2^36 values: below 2^24 of them
     auto run = [&](auto at, auto ot, auto act) {
         constexpr int AT = decltype(at)::value, OT = decltype(ot)::value, ACT = decltype(act)::value;
         if (rows == 16)

@@ -20,8 +20,8 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_expert(ExpertArgs p, int out_
     const Works<C::PB> works(p.offsets, p.G, p.M, nblocks);
     // workgroup b runs on XCD b % 8: each XCD takes one contiguous run of the work
     const int per = (works.total + 7) >> 3;
-    const int jx = (int)(blockIdx.x >> 3);
-    const int wk = (int)(blockIdx.x & 7) * per + jx;
+    const int jx = workgroup() >> 3;
+    const int wk = (workgroup() & 7) * per + jx;
     if (jx >= per || wk >= works.total) return;
     const Work tl = works.at(wk);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -80,8 +80,7 @@ hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
     constexpr int COLS = GATED ? C::PA / 2 : C::PA;
     const int nblocks = ((GATED ? p.N / 2 : p.N) + COLS - 1) / COLS;
     const int64_t grid = (nblocks * most_tiles(p.M, p.G, p.offsets, C::PB) + 7) / 8 * 8;
-    if (!launchable(grid, C::WAVES)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_expert<C, AT, GATED>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, p, out_at, nblocks);
+    hipLaunchKernelGGL((k_expert<C, AT, GATED>), grid_of(grid), dim3(64 * C::WAVES), 0, s, p, out_at, nblocks);
     return hipGetLastError();
 }
 

@@ -18,8 +18,8 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_expert_rows(ExpertGradArgs p,
     __shared__ __align__(1024) char lds[kCoreLds<C>];
     const Works<C::PB> works(p.offsets, p.G, p.M, nblocks);
     const int per = (works.total + 7) >> 3;                // as in the forward product
-    const int jx = (int)(blockIdx.x >> 3);
-    const int wk = (int)(blockIdx.x & 7) * per + jx;
+    const int jx = workgroup() >> 3;
+    const int wk = (workgroup() & 7) * per + jx;
     if (jx >= per || wk >= works.total) return;
     const Work tl = works.at(wk);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -45,9 +45,9 @@ __global__ __launch_bounds__(64 * C::WAVES) void k_expert_matrices(ExpertGradArg
     // Groups differ in rows, and a tile's time with them: every XCD (workgroup b runs on XCD b % 8) takes a
     // share of each group, its column blocks of x where there are eight.  One run of groups to each XCD
     // took 331 us where this takes 273 (64 groups of 256 rows, 2048 x 2048).
-    const int64_t wk = blockIdx.x;
-    const int split = (int)(wk / tiles) % splits, group = (int)(wk / tiles / splits);
-    const int nb = (int)(wk % tiles) / kblocks, kb = (int)(wk % tiles) % kblocks;
+    const int wk = workgroup(), split = wk / tiles % splits, group = wk / tiles / splits;
+    if (group >= p.G) return;
+    const int nb = wk % tiles / kblocks, kb = wk % tiles % kblocks;
     int lo = 0, hi = p.M;
     if (p.offsets) {
         lo = min(max(p.offsets[group], 0), p.M);
@@ -98,8 +98,7 @@ template <class C, int AT>
 hipError_t rows(const ExpertGradArgs& p, hipStream_t s) {
     const int nblocks = (p.K + C::PA - 1) / C::PA;
     const int64_t grid = (nblocks * most_tiles(p.M, p.G, p.offsets, C::PB) + 7) / 8 * 8;
-    if (!launchable(grid, C::WAVES)) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_expert_rows<C, AT>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, p, nblocks);
+    hipLaunchKernelGGL((k_expert_rows<C, AT>), grid_of(grid), dim3(64 * C::WAVES), 0, s, p, nblocks);
     return hipGetLastError();
 }
 
@@ -109,8 +108,7 @@ hipError_t matrices(const ExpertGradArgs& p, int dw_at, hipStream_t s) {
         typedef decltype(tile) C;
         const int kblocks = (p.K + C::PA - 1) / C::PA, tiles = kblocks * ((p.N + C::PB - 1) / C::PB);
         const int64_t grid = (int64_t)tiles * splits * p.G;
-        if (!launchable(grid, C::WAVES)) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((k_expert_matrices<C, AT>), dim3((unsigned)grid), dim3(64 * C::WAVES), 0, s, p, dw_at, kblocks, tiles,
+        hipLaunchKernelGGL((k_expert_matrices<C, AT>), grid_of(grid), dim3(64 * C::WAVES), 0, s, p, dw_at, kblocks, tiles,
                            splits);
         if (splits > 1) {
             if (const hipError_t e = hipGetLastError()) return e;

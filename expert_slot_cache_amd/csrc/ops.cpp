@@ -15,8 +15,8 @@ void set_last_error(const char* msg);   // moe_pool.cpp
 
 namespace {
 
-// A launch has fewer than 2^32 lanes: 256 for each token, or 512 for 2^15 elements of a product
-// and the short last tiles of its groups.
+// A launch has fewer than 2^32 lanes: 256 for each token, or 512 for 2^15 elements of an e4m3 product and the
+// short last tiles of its groups (the other products lay their workgroups in two dimensions where they are more).
 constexpr int64_t kMaxPairs = (int64_t)1 << 24;
 constexpr int32_t kMaxTokens = (1 << 24) - 1;
 constexpr int64_t kMaxElements = (int64_t)1 << 36;

@@ -4,7 +4,16 @@
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
+#include "product_tile.hpp"
+
 namespace moe {
+
+// A launch of that many workgroups, and this one's number in it.
+inline dim3 grid_of(int64_t workgroups) {
+    if (workgroups <= kGridRow) return dim3((unsigned)workgroups);
+    return dim3(kGridRow, (unsigned)grid_rows(workgroups));
+}
+__device__ __forceinline__ int workgroup() { return (int)(blockIdx.x + blockIdx.y * kGridRow); }
 
 // The work: the row tiles of all groups, TM rows each, times the column blocks of the matrix.
 // Every wave counts the tiles for itself: a lane takes a run of groups, a prefix over the lanes
