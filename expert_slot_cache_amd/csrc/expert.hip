@@ -86,7 +86,7 @@ hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
 
 template <int AT, bool GATED>
 hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
-    return expert_tile<GATED>(AT == A_BF16, p.M, p.G, p.N, p.offsets, [&](auto tile) { return expert<decltype(tile), AT, GATED>(p, out_at, s); });
+    return expert_tile<GATED>(std::integral_constant<bool, AT == A_BF16>{}, p.M, p.G, p.N, p.offsets, [&](auto tile) { return expert<decltype(tile), AT, GATED>(p, out_at, s); });
 }
 
 }  // namespace

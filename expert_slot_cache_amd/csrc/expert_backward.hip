@@ -103,6 +103,12 @@ hipError_t rows(const ExpertGradArgs& p, hipStream_t s) {
 }
 
 template <int AT>
+hipError_t rows(const ExpertGradArgs& p, hipStream_t s) {
+    return expert_tile<false>(std::integral_constant<bool, AT == A_BF16>{}, p.M, p.G, p.K, p.offsets,
+                              [&](auto tile) { return rows<decltype(tile), AT>(p, s); });
+}
+
+template <int AT>
 hipError_t matrices(const ExpertGradArgs& p, int dw_at, hipStream_t s) {
     return matrix_tile(p.M, p.G, p.N, p.K, [&](auto tile, int splits) {
         typedef decltype(tile) C;
@@ -128,10 +134,7 @@ size_t expert_backward_workspace(int atype, int M, int G, int N, int K) {
 
 hipError_t launch_expert_backward(int atype, int dw_atype, const ExpertGradArgs& p, hipStream_t s) {
     if (p.dx && p.M > 0) {
-        const hipError_t e = expert_tile<false>(atype == A_BF16, p.M, p.G, p.K, p.offsets, [&](auto tile) {
-            typedef decltype(tile) C;
-            return atype == A_F32 ? rows<C, A_F32>(p, s) : rows<C, A_BF16>(p, s);
-        });
+        const hipError_t e = atype == A_F32 ? rows<A_F32>(p, s) : rows<A_BF16>(p, s);
         if (e) return e;
     }
     if (!p.dw) return hipSuccess;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 namespace moe {
 
@@ -91,15 +92,20 @@ struct CoreTile {
 //   fp32, 64 x 32 / 32 x 32    333 x 1000 (176 tiles): 15.1 / 13.8;  64 rows (64 tiles): 24.3 / 15.0;
 //                           64 groups of 16 rows, 1024 x 1024: 64 / 58;  one row each: 35.3 / 35.2
 // (fp32's products take sixteen times as long: larger tiles gain nothing).  SwiGLU's small
-// tiles have two waves instead of four: a wave's fragments are gate and up.
-template <bool SWIGLU, class F>
-auto expert_tile(bool bf16, int64_t M, int64_t G, int64_t N, bool offsets, F f) {
+// tiles have two waves instead of four: a wave's fragments are gate and up.  Where bf16 is the
+// constant std::false_type, f is asked for no tile that fp32 does not take.
+template <bool SWIGLU, class Bf16, class F>
+auto expert_tile(Bf16 bf16, int64_t M, int64_t G, int64_t N, bool offsets, F f) {
+    constexpr bool kAny = !std::is_same<Bf16, std::false_type>::value;
     const int64_t avg = M / G;
     auto fills = [&](int PA, int PB, int64_t least) { return (N + PA - 1) / PA * most_tiles(M, G, offsets, PB) >= least; };
     constexpr int64_t kMost = 192;
-    if (bf16 && avg >= 384 && fills(256, 256, kMost)) return f(CoreTile<256, 256, 2, 4, 32, 128, 2>{});
-    if (bf16 && avg >= 128 && fills(256, 128, kMost)) return f(CoreTile<256, 128, 4, 2, 32, 128, 3>{});
-    if ((bf16 ? avg >= 48 : SWIGLU && avg >= 768) && fills(128, 64, kMost)) return f(CoreTile<128, 64, 2, 2, 32, 128, 3>{});
+    if constexpr (kAny) {
+        if (bf16 && avg >= 384 && fills(256, 256, kMost)) return f(CoreTile<256, 256, 2, 4, 32, 128, 2>{});
+        if (bf16 && avg >= 128 && fills(256, 128, kMost)) return f(CoreTile<256, 128, 4, 2, 32, 128, 3>{});
+    }
+    if constexpr (kAny || SWIGLU)
+        if ((bf16 ? avg >= 48 : SWIGLU && avg >= 768) && fills(128, 64, kMost)) return f(CoreTile<128, 64, 2, 2, 32, 128, 3>{});
     if (avg >= 32 && fills(64, 64, kMost)) return f(CoreTile<64, 64, SWIGLU ? 1 : 2, 2, 32, 128, SWIGLU ? 4 : 3>{});
     if (fills(64, 32, bf16 ? 128 : 256)) return f(CoreTile<64, 32, 2, 2, 16, 128, 4>{});
     return f(CoreTile<32, 32, SWIGLU ? 1 : 2, 2, 16, 128, 6>{});
