@@ -127,7 +127,7 @@ hipError_t matrices(const ExpertGradArgs& p, int dw_at, hipStream_t s) {
 
 }  // namespace
 
-size_t expert_backward_workspace(int atype, int M, int G, int N, int K) {
+size_t expert_backward_workspace(int M, int G, int N, int K) {
     const int splits = matrix_tile(M, G, N, K, [](auto, int n) { return n; });
     return splits > 1 ? (size_t)splits * G * N * K * sizeof(float) : 0;
 }

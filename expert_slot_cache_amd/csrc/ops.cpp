@@ -294,8 +294,8 @@ moe_status_t moe_expert_product(int32_t atype, const void* x_dev, const void* w_
 }
 
 size_t moe_activation_backward_workspace_bytes(int32_t n_rows, int32_t n_groups, int32_t n_cols) {
-    if (n_rows < 0 || n_rows > kMaxPairs || n_groups < 1 || n_groups > moe::kMaxExperts || n_cols < 1 || n_cols > 2 * kMaxHidden)
-        return 0;
+    const int32_t any = 0;
+    if (check_product(MOE_A_F32, n_rows, n_groups, &any, n_cols, 4)) return 0;   // the format with the smallest pieces
     return moe::activation_workspace(n_rows, n_groups, n_cols);
 }
 
@@ -322,7 +322,7 @@ size_t moe_expert_product_backward_workspace_bytes(int32_t atype, int32_t n_rows
                                                    int32_t depth) {
     const int32_t any = 0;
     if (check_product(atype, n_rows, n_groups, &any, n_cols, depth)) return 0;
-    return moe::expert_backward_workspace(atype, n_rows, n_groups, n_cols, depth);
+    return moe::expert_backward_workspace(n_rows, n_groups, n_cols, depth);
 }
 
 moe_status_t moe_expert_product_backward(int32_t atype, const void* d_pre_dev, const void* x_dev, const void* w_dev,
@@ -336,7 +336,7 @@ moe_status_t moe_expert_product_backward(int32_t atype, const void* d_pre_dev, c
     if (n_rows == 0 && !d_w_dev) return MOE_OK;
     CHECK(n_rows == 0 || (!bad(d_pre_dev, 16) && (!d_x_dev || !bad(w_dev, 16)) && (!d_w_dev || !bad(x_dev, 16))),
           "null or misaligned buffer (16 bytes)");
-    const size_t need = d_w_dev ? moe::expert_backward_workspace(atype, n_rows, n_groups, n_cols, depth) : 0;
+    const size_t need = d_w_dev ? moe::expert_backward_workspace(n_rows, n_groups, n_cols, depth) : 0;
     CHECK(need == 0 || (!bad(workspace_dev, 16) && workspace_bytes >= need), "this gradient needs %zu bytes of workspace", need);
     const moe::ExpertGradArgs a{d_pre_dev, x_dev, w_dev, offsets_dev, d_x_dev, d_w_dev, static_cast<float*>(workspace_dev),
                                 n_rows, n_groups, n_cols, depth};

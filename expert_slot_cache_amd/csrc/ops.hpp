@@ -98,7 +98,7 @@ hipError_t launch_activation_backward(int atype, int out_atype, const Activation
 
 // ---- expert_backward.hip ----
 // Bytes of the partial sums of the matrices' gradients (0: none are needed).
-size_t expert_backward_workspace(int atype, int M, int G, int N, int K);
+size_t expert_backward_workspace(int M, int G, int N, int K);
 struct ExpertGradArgs {
     const void* dpre;         // [M][N]
     const void* x;            // [M][K], for dw

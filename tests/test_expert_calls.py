@@ -37,3 +37,11 @@ def test_other_types_are_refused(on_cpu, call, name, kind):  # noqa: F811
     good = tensors(call)
     with pytest.raises(binding.MoeError):
         getattr(binding, call)(**dict(good, **{name: good[name].to(kind)}))
+
+
+def test_a_workspace_for_sizes_that_are_refused_is_none():
+    f = binding.activation_backward_workspace_bytes
+    assert f(100, 4, 64) > 0 and f(100, 4, 4) > 0      # 4 columns are a piece of fp32
+    assert f(100, 4, 5) == 0 and f(100, 4, 62) == 0    # no format has such rows
+    assert f(1 << 24, 1, 1 << 12) > 0 and f(1 << 24, 1, 1 << 13) == 0    # 2^36 values are the most
+    assert f(100, 4, (1 << 18) + 4) == 0 and f((1 << 24) + 1, 4, 64) == 0 and f(100, 4097, 64) == 0
