@@ -90,7 +90,8 @@ struct CoreTile {
 //                           with the 64 x 64 of SwiGLU: 1075 / 1215 and 324 / 357
 //   fp32, 64 x 64 / 64 x 32    8 groups of 512 rows: 290 / 298;  64 of 16 rows, 1024 x 1024: 91 / 64
 //   fp32, 64 x 32 / 32 x 32    333 x 1000 (176 tiles): 15.1 / 13.8;  64 rows (64 tiles): 24.3 / 15.0;
-//                           64 groups of 16 rows, 1024 x 1024: 64 / 58;  one row each: 35.3 / 35.2
+//                           64 groups of 16 rows, 1024 x 1024: 64 / 58, back to the rows 58 / 64;  of 8 rows,
+//                           1024 x 2048: 97 / 93, 96 / 99;  of 2 rows: 80 / 77, 74 / 79 (one rule for both ways)
 // (fp32's products take sixteen times as long: larger tiles gain nothing).  SwiGLU's small
 // tiles have two waves instead of four: a wave's fragments are gate and up.  Where bf16 is the
 // constant std::false_type, f is asked for no tile that fp32 does not take.
@@ -112,13 +113,20 @@ auto expert_tile(Bf16 bf16, int64_t M, int64_t G, int64_t N, bool offsets, F f) 
 }
 
 // f of the tile of a matrix' gradient, N x K for each group, and of the parts that a group's rows are
-// split into where the tiles are too few for 256 CUs.  Measured as above:
+// split into where the tiles are too few for 256 CUs.  Measured as above, in bf16:
 //   256 x 256 / 256 x 128   64 groups: 512 rows each 427 / 433, 256 rows 333 / 331, 8 rows 145 / 130;
 //                           one group of 8192 rows, 4096 x 4096: 211 / 241
 //   256 x 128 / 128 x 128   64 groups of 256 rows: 331 / 368;  one of 8192 rows (128 / 256 tiles): 103 / 83
 //   128 x 128 / 128 x 64    one group of 2048 rows, 1024 x 1024 (64 / 128 tiles): 23 / 16
 //   parts 1, 2, 4, 8, 16    one group, 64 x 2048 (16 tiles): 16384 rows 86, -, -, 20.0, 20.9;  4096 rows
-//                           25, 16, 14.2, 14.2, -;  1024 rows 9.8, -, 12.9;  2048 rows, 1024 x 1024: 15.7, 18.3
+//                           25, 16, 14.2, 14.2, -;  1024 rows 9.8, -, 12.9;  2048 rows, 1024 x 1024: 15.7, 18.3;
+//                           64 x 2048 again: 4095 rows 25, 17, 13.1, 13.1;  3000 rows 19.5, 14.3, 12.4;
+//                           2048 rows 14.7, 12.3, 12.5;  1500 rows 11.8, 11.4;  1024 rows 10.8, 12.7
+// A part keeps 2048 rows, so a call of few columns between 1500 and 8191 rows takes up to 12 us more than with
+// four parts.  fp32 takes the same tiles and parts, and would gain from smaller and from more of them:
+//   256 x 128 / 128 x 128   64 groups: 256 rows each, 2048 x 2048: 1122 / 1088;  512 rows, 1024 x 2048: 1258 / 1138
+//   128 x 128 / 128 x 64    one group of 8192 rows, 2048 x 2048: 527 / 491
+//   parts 1, 2, 4, 8        64 x 2048: 16384 rows 529, 270, 142, 78;  4096 rows 135, 73, 41, 27;  2048 rows 71, 40, 24, 18
 template <class F>
 auto matrix_tile(int64_t M, int64_t G, int64_t N, int64_t K, F f) {
     const int64_t avg = M / G;

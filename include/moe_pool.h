@@ -503,7 +503,10 @@ moe_status_t moe_route_backward(int32_t atype, const void* logits_dev, int64_t l
  * expert whose logit or bias is -inf or NaN is masked: it is chosen only when nothing else is
  * left in the kept groups (in ascending id order), does not count in its group's sum, and a
  * group of masked experts alone is kept only when no other is left; the score of a logit of -inf
- * or NaN is 0.  Weights whose sum is 0 are 0.  Errors: EINVAL, EHIP. */
+ * or NaN is 0.  Weights whose sum is 0 are 0.  Weights are taken in fp32: off by at most
+ * (3 D + n_experts + top_k + 16) 2^-24 of themselves, D the largest difference of two of the token's
+ * finite logits (sigmoid: twice the largest |l|), and scale 2^-125.
+ * Errors: EINVAL, EHIP. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
 moe_status_t moe_route_groups(int32_t atype, const void* logits_dev, int64_t logits_stride, const float* bias_dev,
@@ -596,7 +599,9 @@ moe_status_t moe_scaled_product(const void* x_dev, const float* x_scales_dev, co
 /* Sorted rows times their group's matrix in the activation format, with bias, activation and
  * residual in the epilogue; group g has the rows offsets[g] .. offsets[g+1]:
  *   h = x[r] w[g]^T + bias[g],   out[r] = act(h) + resid[r]
- * Products of bf16 values are exact; sums are fp32, and each output is rounded once from them.
+ * Products of bf16 values are exact; sums are fp32, and each output is rounded once from them.  A sum of n
+ * terms is off by at most 2 (n + 4) 2^-24 of the sum of their magnitudes; an activation adds, of its value
+ * and besides |h| 2^-125, (2 |h| + 8) 2^-24 (SiLU) or (h^2 + 20) 2^-24 (GELU).
  *  x_dev         [n_rows][depth] and w_dev [n_groups][n_cols][depth] in the activation format;
  *                n_cols and depth multiples of 8 (fp32: 4); n_rows <= 2^24, at most 2^36 elements
  *                in w_dev and in any array of rows.
@@ -632,7 +637,9 @@ moe_status_t moe_expert_product(int32_t atype, const void* x_dev, const void* w_
  *                MOE_ACT_NONE in the same format d_out_dev.
  *  workspace_dev moe_activation_backward_workspace_bytes(n_rows, n_groups, n_cols) bytes on 16
  *                where d_bias_dev is given, used by this call only.
- * act' at NaN is NaN, relu's at 0 is 0.  A group without rows has a d_bias of 0 (n_rows = 0 as well).
+ * act' at NaN is NaN, relu's at 0 is 0.  A bias' sum is fp32 over up to 64 rows and fp64 over those: off by
+ * at most 18 2^-24 of the sum of the magnitudes, however many rows there are.  A group without rows has
+ * a d_bias of 0 (n_rows = 0 as well).
  * Sizes, offsets, alignment and the rows outside every group as in moe_expert_product.
  * Errors: EINVAL, EHIP. */
 moe_status_t moe_activation_backward(int32_t atype, const void* d_out_dev, int32_t out_atype, const void* pre_dev,
