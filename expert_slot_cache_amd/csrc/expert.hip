@@ -80,7 +80,7 @@ hipError_t expert(const ExpertArgs& p, int out_at, hipStream_t s) {
     constexpr int COLS = GATED ? C::PA / 2 : C::PA;
     const int nblocks = ((GATED ? p.N / 2 : p.N) + COLS - 1) / COLS;
     const int64_t grid = (nblocks * most_tiles(p.M, p.G, p.offsets, C::PB) + 7) / 8 * 8;
-    hipLaunchKernelGGL((k_expert<C, AT, GATED>), grid_of(grid), dim3(64 * C::WAVES), 0, s, p, out_at, nblocks);
+    hipLaunchKernelGGL((k_expert<C, AT, GATED>), blocks_of(grid, C::WAVES), dim3(64 * C::WAVES), 0, s, p, out_at, nblocks);
     return hipGetLastError();
 }
 

@@ -98,7 +98,7 @@ template <class C, int AT>
 hipError_t rows(const ExpertGradArgs& p, hipStream_t s) {
     const int nblocks = (p.K + C::PA - 1) / C::PA;
     const int64_t grid = (nblocks * most_tiles(p.M, p.G, p.offsets, C::PB) + 7) / 8 * 8;
-    hipLaunchKernelGGL((k_expert_rows<C, AT>), grid_of(grid), dim3(64 * C::WAVES), 0, s, p, nblocks);
+    hipLaunchKernelGGL((k_expert_rows<C, AT>), blocks_of(grid, C::WAVES), dim3(64 * C::WAVES), 0, s, p, nblocks);
     return hipGetLastError();
 }
 
@@ -114,7 +114,7 @@ hipError_t matrices(const ExpertGradArgs& p, int dw_at, hipStream_t s) {
         typedef decltype(tile) C;
         const int kblocks = (p.K + C::PA - 1) / C::PA, tiles = kblocks * ((p.N + C::PB - 1) / C::PB);
         const int64_t grid = (int64_t)tiles * splits * p.G;
-        hipLaunchKernelGGL((k_expert_matrices<C, AT>), grid_of(grid), dim3(64 * C::WAVES), 0, s, p, dw_at, kblocks, tiles,
+        hipLaunchKernelGGL((k_expert_matrices<C, AT>), blocks_of(grid, C::WAVES), dim3(64 * C::WAVES), 0, s, p, dw_at, kblocks, tiles,
                            splits);
         if (splits > 1) {
             if (const hipError_t e = hipGetLastError()) return e;

@@ -51,11 +51,17 @@ auto product_tile(int64_t M, int64_t G, int64_t N, bool offsets, F f) {
 
 // ---- products in the activation format ----
 
-// One dimension of a launch has fewer than 2^32 lanes, so its workgroups (of at most 512) lie in rows of
-// 2^22, of which the last may have some too many: number x + y 2^22.  A multiple of 8, so that the number
-// tells the XCD as x alone does.
-constexpr int kGridRow = 1 << 22;
-inline int64_t grid_rows(int64_t workgroups) { return (workgroups + kGridRow - 1) / kGridRow; }
+// One dimension of a launch has fewer than 2^32 lanes.  More workgroups lie in rows of at most 2^22, of a
+// multiple of 8, so that a workgroup's number, x + y columns, tells its XCD as x alone does; up to 7 of a
+// row have nothing to do.
+struct Grid {
+    int64_t columns, rows;
+};
+inline Grid grid_of(int64_t workgroups, int waves) {
+    if (workgroups * 64 * waves < (int64_t)1 << 32) return {workgroups, 1};
+    const int64_t most = 1 << 22, rows = (workgroups + most - 1) / most;
+    return {((workgroups + rows - 1) / rows + 7) / 8 * 8, rows};
+}
 
 // A workgroup of WA x WB waves computes PA columns x PB rows of the output, in fragments of F x F
 // (the columns are the instruction's A operand, so that four accumulators of a lane are consecutive

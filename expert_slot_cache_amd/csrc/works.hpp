@@ -9,11 +9,11 @@
 namespace moe {
 
 // A launch of that many workgroups, and this one's number in it.
-inline dim3 grid_of(int64_t workgroups) {
-    if (workgroups <= kGridRow) return dim3((unsigned)workgroups);
-    return dim3(kGridRow, (unsigned)grid_rows(workgroups));
+inline dim3 blocks_of(int64_t workgroups, int waves) {
+    const Grid g = grid_of(workgroups, waves);
+    return dim3((unsigned)g.columns, (unsigned)g.rows);
 }
-__device__ __forceinline__ int workgroup() { return (int)(blockIdx.x + blockIdx.y * kGridRow); }
+__device__ __forceinline__ int workgroup() { return (int)(blockIdx.x + blockIdx.y * gridDim.x); }
 
 // The work: the row tiles of all groups, TM rows each, times the column blocks of the matrix.
 // Every wave counts the tiles for itself: a lane takes a run of groups, a prefix over the lanes
