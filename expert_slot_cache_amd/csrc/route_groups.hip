@@ -25,7 +25,7 @@
 // experts, top-10 in fp32, sigmoid, take 17 us without bias and groups, 22 with the 4 best of 8 groups,
 // 30 with a bias: about one token in a thousand is taken again, and the call waits for the last (36 us
 // where each of them was with all of its experts).  Where choices are equal, most tokens are: bf16 logits
-// with one bias for all take 49 us, and logits that are all the same 94, with groups 118.  Masked experts
+// with one bias for all take 50 us, and logits that are all the same 94, with groups 117.  Masked experts
 // cost nothing: next to one the order is in no doubt (28 to 34 us with all but 10 to 20 masked).
 #include <hip/hip_runtime.h>
 
